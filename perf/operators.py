@@ -31,7 +31,7 @@ def listed():
         # one decoded token on its 8 experts of a rank that holds 32: weights stream once, latency counts
         dict(name="experts 8 rows", op="experts", R=8, E=32, d=4096, F=2048, layout="concat", act="silu", bias=False),
         # a decode batch whose rows share experts; odd row count, features that end inside a block, biases
-        dict(name="experts 77 rows, ragged", op="experts", R=77, E=16, d=2880, F=2880, layout="unfused", act="gelu_tanh",
+        dict(name="experts 77 ragged rows", op="experts", R=77, E=16, d=2880, F=2880, layout="unfused", act="gelu_tanh",
              bias=True),
         # a prefill chunk on one rank's share of many small experts
         dict(name="experts 4096 rows", op="experts", R=4096, E=32, d=7168, F=2048, layout="concat", act="silu", bias=False),
