@@ -70,7 +70,7 @@ typedef enum {
 } moe_status;
 
 /* ---- dtype codes ---- */
-enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2 };
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2, MOE_FP8 = 3 };
 /* ---- scoring ("Struct MoeSpec" score) ---- */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 /* ---- gated activation ("Struct MoeSpec" act; graph-op activation_type) ---- */
@@ -87,7 +87,14 @@ enum { MOE_FFN_GATED = 0, MOE_FFN_PLAIN = 1 };
  * F expert dff, E routed experts, k experts per token (1 <= k <= E), Fs the
  * shared expert's dff (0 = no shared expert).
  * Supported dtype combinations (act_dtype, w_dtype): (F32, F32), (BF16, BF16),
- * (BF16, MXFP4).  logit_dtype is F32 or BF16.
+ * (BF16, MXFP4), (BF16, FP8).  logit_dtype is F32 or BF16.
+ *
+ * MOE_FP8: e4m3 expert stacks with one fp32 scale per 128 x 128 block (moe_fp8.h).  The
+ * expert's input rows (weighed ones with weigh_inputs) and its activations h are
+ * quantised on the way, per row and 128 columns, from their fp32 values; products and
+ * biases are fp32, each expert row is rounded to bf16 before the combine (batches whose
+ * down product is split along K: once, after the combine).  d and F multiples of 16;
+ * fused concat, unfused and plain layouts (not interleaved).
  */
 typedef struct {
   int64_t T, d, F, E, k, Fs;
@@ -125,10 +132,13 @@ typedef struct {
  *   selection_bias  [E] fp32, optional
  *   gate_up         [E, 2F, d] w_dtype; MXFP4: e2m1 codes [E, 2F, d/2] u8, two per
  *                   byte, the even k in the low nibble
- *   gate_up_scales  MXFP4 only: e8m0 block scales [E, 2F, d/32] u8 (blocks of 32 along d)
+ *   gate_up_scales  MXFP4: e8m0 block scales [E, 2F, d/32] u8 (blocks of 32 along d);
+ *                   FP8: fp32 scales, passed as their bytes (4-byte aligned): concat
+ *                   [E, 2 ceil(F/128), ceil(d/128)], the gate rows' blocks first (the
+ *                   up rows start a new block), unfused or plain [E, ceil(F/128), ceil(d/128)]
  *   gate_up_bias    [E, 2F] act_dtype, optional (same row order as gate_up)
  *   down            [E, d, F] w_dtype; MXFP4: codes [E, d, F/2]
- *   down_scales     MXFP4 only: [E, d, F/32]
+ *   down_scales     MXFP4: [E, d, F/32]; FP8: fp32 [E, ceil(d/128), ceil(F/128)]
  *   down_bias       [E, d] act_dtype, optional
  *   shared_gate_up  [2Fs, d] act_dtype (required when Fs > 0; same layout option)
  *   shared_down     [d, Fs] act_dtype (required when Fs > 0)
@@ -138,7 +148,8 @@ typedef struct {
  *   topk_idx        [T, k] int32, optional output: chosen experts, best first
  *   topk_w          [T, k] fp32, optional output: their weights
  *   gate            MOE_GU_UNFUSED only: the gate rows [E, F, d] w_dtype (MXFP4: codes
- *                   [E, F, d/2] with gate_scales [E, F, d/32]); gate_up then holds the
+ *                   [E, F, d/2] with gate_scales [E, F, d/32]; FP8: with fp32
+ *                   gate_scales [E, ceil(F/128), ceil(d/128)]); gate_up then holds the
  *                   up rows [E, F, d] and gate_up_bias their bias [E, F]
  *   gate_bias       [E, F] act_dtype, optional (MOE_GU_UNFUSED)
  *   router_weight   [d, E] act_dtype ("Struct MoeSpec" wr, wr[(i-1)E + e]): with
@@ -204,6 +215,8 @@ MOE_API size_t moe_workspace_size(const moe_shape *shape, const moe_options *opt
  *     MOE_B200_FUSED_FFN=0 or MOE_B200_INTERLEAVE=1, gate_up and down run as one
  *     launch whose down tiles start once their expert's h rows are complete (a
  *     cooperative launch; where its CTAs cannot all be resident, two launches);
+ *   - FP8 weights: 128-row tiles, one CTA per tile, split along K when the tiles leave
+ *     SMs idle; a shared expert (bf16) beside them as beside MXFP4 experts;
  *   - MXFP4 weights: one CTA per tile; MOE_B200_PAIR_FP4=1 picks CTA pairs with
  *     256 decoded weight rows (slower on the shapes measured);
  *   - MOE_B200_INTERLEAVE=1: the bf16 GEMMs visit the experts largest first,

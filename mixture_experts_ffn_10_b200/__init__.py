@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN = 0, 1, 2, 3, 4
 MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_ARG = 5, 6, 7, 8, 9
-MOE_F32, MOE_BF16, MOE_MXFP4 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_MXFP4, MOE_FP8 = 0, 1, 2, 3
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ACT_SILU, MOE_ACT_GELU_ERF, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_IDENTITY = 0, 1, 2, 3, 4
 MOE_GU_CONCAT, MOE_GU_INTERLEAVED, MOE_GU_UNFUSED = 0, 1, 2
@@ -30,7 +30,7 @@ MOE_FFN_GATED, MOE_FFN_PLAIN = 0, 1
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_DTYPE",
                 4: "MOE_ERR_ALIGN", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_WORKSPACE",
                 7: "MOE_ERR_CUDA", 8: "MOE_ERR_TIMEOUT", 9: "MOE_ERR_ARG"}
-DTYPE_CODES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4}
+DTYPE_CODES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4, "fp8": MOE_FP8}
 SCORE_CODES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 ACT_CODES = {"silu": MOE_ACT_SILU, "gelu_erf": MOE_ACT_GELU_ERF, "gelu_tanh": MOE_ACT_GELU_TANH,
              "relu": MOE_ACT_RELU, "identity": MOE_ACT_IDENTITY}

@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "ep.cuh"
+#include "fp8.cuh"
 #include "moe_ep.h"
 #include "gemv.cuh"
 
@@ -51,9 +52,10 @@ int check_shape_opts(const moe_shape* s, const moe_options* o) {
     return fail(MOE_ERR_DTYPE, "logit_dtype %d must be MOE_F32 or MOE_BF16", s->logit_dtype);
   const bool combo = (s->act_dtype == MOE_F32 && s->w_dtype == MOE_F32) ||
                      (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_BF16) ||
-                     (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_MXFP4);
+                     (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_MXFP4) ||
+                     (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_FP8);
   if (!combo)
-    return fail(MOE_ERR_DTYPE, "(act_dtype, w_dtype) = (%d, %d): supported are (F32,F32), (BF16,BF16), (BF16,MXFP4)",
+    return fail(MOE_ERR_DTYPE, "(act_dtype, w_dtype) = (%d, %d): supported are (F32,F32), (BF16,BF16), (BF16,MXFP4), (BF16,FP8)",
                 s->act_dtype, s->w_dtype);
   if (s->T < 0 || s->d < 8 || s->F < 8 || s->E < 1 || s->Fs < 0)
     return fail(MOE_ERR_SHAPE, "need T >= 0, d >= 8, F >= 8, E >= 1, Fs >= 0 (got T=%lld d=%lld F=%lld E=%lld Fs=%lld)",
@@ -65,6 +67,8 @@ int check_shape_opts(const moe_shape* s, const moe_options* o) {
     return fail(MOE_ERR_SHAPE, "d, F and Fs must be multiples of 8 (16-byte rows)");
   if (s->w_dtype == MOE_MXFP4 && (s->d % 32 || s->F % 32))
     return fail(MOE_ERR_SHAPE, "MXFP4 experts need d and F multiples of 32 (block size)");
+  if (s->w_dtype == MOE_FP8 && (s->d % kFp8MinNK || s->F % kFp8MinNK))
+    return fail(MOE_ERR_SHAPE, "FP8 experts need d and F multiples of 16 (16-byte rows)");
   const int64_t rows = s->T * s->k + (s->Fs > 0 ? s->T : 0);
   if (s->T > (1ll << 26) || rows >= (1ll << 31))
     return fail(MOE_ERR_SHAPE, "T*k + T must stay below 2^31 rows (T=%lld)", (long long)s->T);
@@ -74,6 +78,8 @@ int check_shape_opts(const moe_shape* s, const moe_options* o) {
   if (o->gu_layout != MOE_GU_CONCAT && o->gu_layout != MOE_GU_INTERLEAVED && o->gu_layout != MOE_GU_UNFUSED)
     return fail(MOE_ERR_ARG, "gu_layout %d", o->gu_layout);
   if (o->ffn != MOE_FFN_GATED && o->ffn != MOE_FFN_PLAIN) return fail(MOE_ERR_ARG, "ffn %d", o->ffn);
+  if (s->w_dtype == MOE_FP8 && o->gu_layout == MOE_GU_INTERLEAVED && o->ffn == MOE_FFN_GATED)
+    return fail(MOE_ERR_UNSUPPORTED, "FP8 experts take the concat, unfused and plain layouts (128 features per scale)");
   if (o->ffn == MOE_FFN_PLAIN && o->gu_layout == MOE_GU_UNFUSED)
     return fail(MOE_ERR_ARG, "an unfused gate stack needs a gated FFN (ffn = MOE_FFN_GATED)");
   if ((o->renormalize & ~1) || (o->weigh_inputs & ~1) || (o->shared_gate & ~1))
@@ -118,6 +124,13 @@ int check_tensors(const moe_shape* s, const moe_options* o, const moe_tensors* t
   if (o->gu_layout == MOE_GU_UNFUSED && !t->gate) return fail(MOE_ERR_NULL, "the unfused layout needs gate");
   if (o->gu_layout == MOE_GU_UNFUSED && s->w_dtype == MOE_MXFP4 && !t->gate_scales)
     return fail(MOE_ERR_NULL, "unfused MXFP4 experts need gate_scales");
+  if (s->w_dtype == MOE_FP8) {
+    const bool unfused = o->gu_layout == MOE_GU_UNFUSED;
+    if (!t->gate_up_scales || !t->down_scales || (unfused && !t->gate_scales))
+      return fail(MOE_ERR_NULL, "FP8 experts need gate_up_scales and down_scales (unfused: gate_scales too)");
+    for (const uint8_t* p : {t->gate_up_scales, t->down_scales, t->gate_scales})
+      if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(MOE_ERR_ALIGN, "FP8 scales are fp32 (4-byte aligned)");
+  }
   if (o->gu_layout != MOE_GU_UNFUSED && (t->gate || t->gate_bias))
     return fail(MOE_ERR_ARG, "gate and gate_bias belong to the unfused layout");
   if (s->Fs > 0 && (!t->shared_gate_up || !t->shared_down))
@@ -331,7 +344,14 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
 
   // The rows in expert order: gathered from x, except for small batches on the
   // single-CTA bf16 GEMMs, whose gate_up reads x in place (direct_x).
-  if (!p.direct_x) {
+  const bool fp8 = s->w_dtype == MOE_FP8;
+  const Fp8Regions fr = fp8 ? fp8_regions(p.R, p.d, p.F, p.E) : Fp8Regions{};
+  const size_t fp8_base = p.total - fr.total;  // the FP8 operands end the workspace
+  if (fp8) {
+    const Fp8GatherArgs ga{static_cast<const uint16_t*>(t->x), sa.pos, sa.roww, at<uint8_t>(ws, fp8_base + fr.xq),
+                           at<float>(ws, fp8_base + fr.xs), (int)p.R, (int)p.d, (int)p.T, (int)p.k, o->weigh_inputs, status};
+    if ((e = launch_fp8_gather(ga, st)) != cudaSuccess) return cuda_fail(e, "gather kernel");
+  } else if (!p.direct_x) {
     GatherArgs ga{t->x, sa.pos, sa.roww, at<void>(ws, p.o_x), (int)p.R, (int)p.d, (int)p.T, (int)p.k,
                   s->act_dtype == MOE_BF16, o->weigh_inputs, status};
     if ((e = launch_gather(ga, st)) != cudaSuccess) return cuda_fail(e, "gather kernel");
@@ -380,7 +400,89 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
   if (p.splits_dn > 1) sync += p.max_tiles_dn * kFixRegions;
   int32_t* ready = p.fused_ffn ? sync : nullptr;
 
-  if (p.tc) {
+  if (fp8) {
+    Fp8GemmArgs fa{};
+    fa.mode = o->ffn == MOE_FFN_PLAIN ? FP8_PLAIN : FP8_GATED;
+    fa.E = (int)p.E;
+    fa.R = (int)p.R;
+    fa.K = (int)p.d;
+    fa.N = (int)p.F;
+    fa.cnt = sa.cnt;
+    fa.a = at<uint8_t>(ws, fp8_base + fr.xq);
+    fa.as = at<float>(ws, fp8_base + fr.xs);
+    fa.layout = o->gu_layout;
+    fa.w = static_cast<const uint8_t*>(t->gate_up);
+    fa.ws = reinterpret_cast<const float*>(t->gate_up_scales);
+    fa.wg = static_cast<const uint8_t*>(t->gate);
+    fa.wgs = reinterpret_cast<const float*>(t->gate_scales);
+    fa.bias = static_cast<const uint16_t*>(t->gate_up_bias);
+    fa.gate_bias = static_cast<const uint16_t*>(t->gate_bias);
+    fa.act = gc.act;
+    fa.hq = at<uint8_t>(ws, fp8_base + fr.hq);
+    fa.hs = at<float>(ws, fp8_base + fr.hs);
+    fa.splits = p.splits_gu;
+    fa.partial = gc.partial;
+    fa.pitch = gc.partial_pitch;
+    fa.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fa.mode, p.F));
+    fa.num_sms = num_sms_of_current_device();
+    fa.status = status;
+    // the bf16 shared expert: the CTA-pair bf16 kernel over the shared segment alone
+    TcArgs sh{};
+    sh.x = t->x;
+    sh.sh_gate_up = t->shared_gate_up;
+    sh.sh_down = t->shared_down;
+    sh.h = at<void>(ws, p.o_h);
+    sh.Y = at<void>(ws, p.o_y);
+    sh.num_sms = fa.num_sms;
+    int32_t* sh_tiles = at<int32_t>(ws, fp8_base + fr.tiles);
+    auto shared_gemm = [&](int nt) -> GemmCommon {
+      GemmCommon c = gc;
+      c.seg_begin = (int)p.E;
+      c.tiles = sh_tiles;
+      c.order = nullptr;
+      c.max_tiles = (int)(mt_shared * nt);
+      return c;
+    };
+    if ((e = launch_fp8_gemm(fa, st)) != cudaSuccess) return cuda_fail(e, "FP8 gate_up GEMM");
+    if (fa.splits > 1 && (e = launch_fp8_reduce_h(fa, sa.off, st)) != cudaSuccess) return cuda_fail(e, "FP8 h reduction");
+    if (p.Fs > 0) {
+      sh.c = shared_gemm(p.nt_gu_shared);
+      if ((e = launch_shared_tiles(sh_tiles, (int)p.E, sh.c.max_tiles, st)) != cudaSuccess)
+        return cuda_fail(e, "shared tile list");
+      if ((e = launch_tc2_gate_up(sh, st)) != cudaSuccess) return cuda_fail(e, "shared expert gate_up GEMM");
+    }
+    if ((e = mark(4)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+    Fp8GemmArgs fd = fa;
+    fd.mode = FP8_LINEAR;
+    fd.K = (int)p.F;
+    fd.N = (int)p.d;
+    fd.a = fa.hq;
+    fd.as = fa.hs;
+    fd.w = static_cast<const uint8_t*>(t->down);
+    fd.ws = reinterpret_cast<const float*>(t->down_scales);
+    fd.bias = static_cast<const uint16_t*>(t->down_bias);
+    fd.gate_bias = nullptr;
+    fd.roww = o->weigh_inputs ? nullptr : sa.roww;
+    fd.y = at<uint16_t>(ws, p.o_y);
+    fd.splits = p.splits_dn;
+    fd.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fd.mode, p.d));
+    if ((e = launch_fp8_gemm(fd, st)) != cudaSuccess) return cuda_fail(e, "FP8 down GEMM");
+    if (p.Fs > 0) {
+      sh.c = shared_gemm(p.nt_dn_shared);
+      if ((e = launch_shared_tiles(sh_tiles, (int)p.E, sh.c.max_tiles, st)) != cudaSuccess)
+        return cuda_fail(e, "shared tile list");
+      if ((e = launch_tc2_down(sh, st)) != cudaSuccess) return cuda_fail(e, "shared expert down GEMM");
+    }
+    if (fd.splits > 1) {
+      if ((e = mark(5)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+      const Fp8CombineArgs ca{fd.partial, fd.splits, fd.pitch, sa.pos, ra.idx, fd.roww, fd.bias, ra.sgate,
+                              p.Fs > 0 ? fd.y + p.R * p.d : nullptr, static_cast<const uint16_t*>(t->shared_output),
+                              static_cast<uint16_t*>(t->y), (int)p.T, (int)p.d, (int)p.k, (int)p.R, (int)p.E, status};
+      if ((e = launch_fp8_combine(ca, st)) != cudaSuccess) return cuda_fail(e, "combine kernel");
+      if ((e = mark(6)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+      return MOE_OK;
+    }
+  } else if (p.tc) {
     TcArgs ta{};
     ta.x = t->x;
     ta.xg = at<void>(ws, p.o_x);
@@ -575,6 +677,8 @@ int forward_on_workspace(const moe_shape* s, const moe_options* o, const moe_ten
 
 int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
+int device_sms() { return num_sms_of_current_device(); }
+
 // CTA-pair GEMMs for large batches with bf16 weights: every expert then has
 // several 256-row tiles on average, and the pair kernel needs a third less TMA
 // traffic per SM.  MOE_B200_PAIR_GEMM=0 or 1 overrides the choice.
@@ -700,6 +804,14 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
     // 128 gated (256 plain) features, or of 256 outputs
     p->nt_gu_shared = (int)cdiv(s->Fs, kTcGuBN * plain);
     p->nt_dn_shared = (int)cdiv(s->d, kTcDnBN);
+  } else if (s->w_dtype == MOE_FP8) {
+    // the FP8 GEMMs make their own tile list from the segments' row counts; the shared
+    // expert (bf16) runs on the CTA-pair bf16 kernel
+    p->bm = kPairBM;
+    p->nt_gu_routed = fp8_n_tiles(o->ffn == MOE_FFN_PLAIN ? FP8_PLAIN : FP8_GATED, s->F);
+    p->nt_dn_routed = fp8_n_tiles(FP8_LINEAR, s->d);
+    p->nt_gu_shared = (int)cdiv(s->Fs, kTcGuBN * plain);
+    p->nt_dn_shared = (int)cdiv(s->d, kTcDnBN);
   } else if (p->swap) {  // pair tiles of 256 weight rows: 128 gated features or 256 plain ones
     p->bm = kSwapBM;
     p->nt_gu_routed = (int)cdiv(s->F, kTcGuBN * plain);
@@ -730,6 +842,14 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
     if (p->splits_gu > 1 || p->splits_dn > 1)
       p->partial_pitch = (int64_t)std::max({p->nt_gu_routed, p->nt_gu_shared, p->nt_dn_routed}) * 256;
   }
+  if (s->w_dtype == MOE_FP8 && p->R > 0) {
+    const int sms = num_sms_of_current_device();
+    const int mode = o->ffn == MOE_FFN_PLAIN ? FP8_PLAIN : FP8_GATED;
+    p->splits_gu = fp8_splits(mode, p->R, p->E, s->F, s->d, sms);
+    p->splits_dn = fp8_splits(FP8_LINEAR, p->R, p->E, s->d, s->F, sms);
+    if (p->splits_gu > 1 || p->splits_dn > 1)
+      p->partial_pitch = (int64_t)std::max(p->nt_gu_routed, p->nt_dn_routed) * 256;
+  }
   // Upper bounds of the GEMMs' tile counts: every non-empty expert adds at most one
   // partial M tile.
   const int64_t mt_routed = p->R / p->bm + std::min<int64_t>(p->E, p->R);
@@ -739,6 +859,7 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
   p->fused_ffn = p->direct_x && !p->interleave && use_fused_ffn();
   p->n_sync = (p->splits_gu > 1 ? p->max_tiles_gu * kFixRegions : 0) +
               (p->splits_dn > 1 ? p->max_tiles_dn * kFixRegions : 0) + (p->fused_ffn ? p->NS : 0);
+  if (s->w_dtype == MOE_FP8) p->n_sync = 0;  // split FP8 products are summed by kernels of their own
   const size_t elt = p->tc ? 2 : 4;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -759,12 +880,14 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
   p->o_perm = take(p->R * 4);
   p->o_roww = take(p->R * 4);
   p->o_sgate = take(p->T * 4);
-  p->o_x = take(p->direct_x ? 0 : p->R * p->d * elt);  // rows in expert order (none for direct_x)
-  p->o_h = take(p->rows * p->Fmax * elt);
+  const bool fp8 = s->w_dtype == MOE_FP8;  // its x and h rows are the FP8 regions at the end
+  p->o_x = take(p->direct_x || fp8 ? 0 : p->R * p->d * elt);  // rows in expert order (none for direct_x)
+  p->o_h = take(fp8 && p->Fs == 0 ? 0 : p->rows * p->Fmax * elt);
   p->o_y = take(p->rows * p->d * elt);
   p->o_part = take((size_t)std::max(p->splits_gu, p->splits_dn) * p->rows * p->partial_pitch * 4 *
                    (p->partial_pitch > 0 ? 1 : 0));
   p->o_sync = take(p->n_sync * 4);
+  if (fp8) take(fp8_regions(p->R, p->d, p->F, p->E).total);
   p->total = off;
   return off;
 }
@@ -836,7 +959,8 @@ int moe_forward_kernel_count(const moe_shape* s, const moe_options* o) {
   // launch with gate_up when fused), combine; a single 64-token chunk sorts in one kernel
   if (moe::gemv_plan(s, p).on) return 1;  // (plus the router GEMM when the layer computes the logits)
   return (p.nchunks == 1 ? 4 : 6) + (p.direct_x ? 0 : 1) + 1 - (p.fused_ffn ? 1 : 0) +
-         (s->w_dtype == MOE_MXFP4 && p.Fs > 0 ? 2 : 0);  // the shared expert beside MXFP4 experts
+         (s->w_dtype == MOE_MXFP4 && p.Fs > 0 ? 2 : 0) +  // the shared expert beside MXFP4 experts
+         (s->w_dtype == MOE_FP8 ? (p.splits_gu > 1) + (p.Fs > 0 ? 4 : 0) : 0);  // the h reduction; tile lists and GEMMs
 }
 
 int moe_forward_split_k(const moe_shape* s, const moe_options* o, int* splits_gate_up, int* splits_down) {

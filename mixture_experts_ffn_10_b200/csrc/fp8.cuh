@@ -1,0 +1,189 @@
+// fp8.cuh -- e4m3 operands with an fp32 scale per block of 128: the rounding to e4m3,
+// and the launchers of the FP8 kernels (quantisation, grouped products, reductions).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kFp8Block = 128;    // columns (and weight rows) that share a scale
+constexpr int kFp8BM = 128;       // rows per tile of the FP8 grouped GEMM (UMMA M)
+constexpr int kFp8MinNK = 16;     // K (and F) multiple: 16-byte rows
+
+// SMs of the current device.
+int device_sms();
+
+// Where an FP8 layer keeps its operands in the workspace (bytes from the region's start).
+struct Fp8Regions {
+  size_t xq, xs, hq, hs, tiles, total;  // tiles: the shared expert's tile prefix [E + 2]
+};
+inline Fp8Regions fp8_regions(int64_t R, int64_t d, int64_t F, int64_t E) {
+  auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+  Fp8Regions r;
+  r.xq = 0;
+  r.xs = up(r.xq + (size_t)R * d);
+  r.hq = up(r.xs + (size_t)R * ((d + 127) / 128) * 4);
+  r.hs = up(r.hq + (size_t)R * F);
+  r.tiles = up(r.hs + (size_t)R * ((F + 127) / 128) * 4);
+  r.total = up(r.tiles + (size_t)(E + 2) * 4);
+  return r;
+}
+// tiles[0 .. E] = 0, tiles[E + 1] = n: the prefix of a tile list that holds the shared
+// segment's n tiles alone (the bf16 shared expert beside FP8 experts).
+cudaError_t launch_shared_tiles(int32_t* tiles, int E, int n, cudaStream_t st);
+
+// ---------------------------------------------------------------- rounding to e4m3
+// The scale of a block of largest magnitude amax.
+__device__ __forceinline__ float fp8_scale(float amax) { return __fdiv_rn(fmaxf(amax, 0x1p-100f), 448.f); }
+
+// A float that the hardware conversion (nearest even, saturating) takes to the e4m3 value
+// nearest to the real quotient x / s; inv = 1 / s rounded.  t = x inv is within two units
+// in the last place of x / s, so the two round alike unless t lies within a few units of
+// a point halfway between e4m3 values.  Such points (and the e4m3 values) have at most
+// four fraction bits: their low 19 bits are zero.  Next to one, m, the residual x - m s
+// (exact in sign in one fma: m s has 29 bits) tells on which side of m the quotient is.
+__device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
+  float t = x * inv;
+  const uint32_t u = __float_as_uint(t) + 8u;
+  if ((u & 0x7ffffu) < 16u) {
+    const uint32_t m = u & ~0x7ffffu;
+    const float r = fmaf(-__uint_as_float(m), s, x);  // NaN (t stays) for NaN x and for infinite s
+    const bool neg = (m >> 31) != 0;
+    if (r == 0.f) t = __uint_as_float(m);
+    if (r > 0.f) t = __uint_as_float(neg ? m - 1u : m + 1u);
+    if (r < 0.f) t = __uint_as_float(neg ? m + 1u : m - 1u);
+  }
+  return t;
+}
+
+// Four quotients as e4m3, the first in the low byte.
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// ---------------------------------------------------------------- activation
+// act(g) in fp32 (h is rounded to e4m3 next to it, a step of 2^-4: the hardware tanh of the
+// bf16 epilogues, 5e-4 off, would move too many values over a rounding border); the SiLU
+// limit applies to gated experts only.
+__device__ __forceinline__ float fp8_act(const ActParams& a, float g, bool gated) {
+  switch (a.act) {
+    case MOE_ACT_SILU:
+      if (gated && a.limit > 0.f) g = fminf(g, a.limit);
+      return __fdividef(g, 1.f + __expf(-a.alpha * g));
+    case MOE_ACT_GELU_ERF: return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+    case MOE_ACT_GELU_TANH: {  // 0.5 (1 + tanh z) = sigmoid(2 z)
+      const float z2 = 2.f * 0.79788456080286536f * fmaf(0.044715f * g, g * g, g);
+      return __fdividef(g, 1.f + __expf(-z2));
+    }
+    case MOE_ACT_RELU: return fmaxf(g, 0.f);
+    default: return g;
+  }
+}
+__device__ __forceinline__ float fp8_up(const ActParams& a, float u) {
+  return a.act == MOE_ACT_SILU && a.limit > 0.f ? fminf(fmaxf(u, -a.limit), a.limit) : u;
+}
+
+// Bias rows of group e: of the gate (or plain) and of the up values; null if absent.
+struct Fp8Bias {
+  const uint16_t *g, *u;
+};
+__device__ __forceinline__ Fp8Bias fp8_bias(int mode, int layout, int e, int64_t N, const uint16_t* bias,
+                                            const uint16_t* gate_bias) {
+  if (mode != 0 /*FP8_GATED*/) return Fp8Bias{bias ? bias + e * N : nullptr, nullptr};
+  if (layout == MOE_GU_UNFUSED)
+    return Fp8Bias{gate_bias ? gate_bias + e * N : nullptr, bias ? bias + e * N : nullptr};
+  return Fp8Bias{bias ? bias + 2 * e * N : nullptr, bias ? bias + (2 * e + 1) * N : nullptr};
+}
+
+// ---------------------------------------------------------------- quantisation
+cudaError_t launch_fp8_quantize(int bf16, int64_t rows, int64_t K, const void* x, int64_t pitch, uint8_t* q,
+                                float* scales, cudaStream_t st);
+cudaError_t launch_fp8_quantize_weights(int bf16, int64_t E, int64_t N, int64_t K, const void* w, uint8_t* q,
+                                        float* scales, cudaStream_t st);
+
+// Row pos[t, j] of xq / xs = x[t] quantised (times the row's weight for weigh-inputs).
+struct Fp8GatherArgs {
+  const uint16_t* x;    // [T, d] bf16
+  const int32_t* pos;   // [T, k]
+  const float* roww;    // [R]
+  uint8_t* xq;          // [R, d]
+  float* xs;            // [R, ceil(d / 128)]
+  int R, d, T, k, weigh_inputs;
+  int* status;
+};
+cudaError_t launch_fp8_gather(const Fp8GatherArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- grouped products
+enum { FP8_GATED = 0, FP8_PLAIN = 1, FP8_LINEAR = 2 };  // what the epilogue makes of the accumulators
+
+// One grouped GEMM: rows of group e are the cnt[e] rows after those of groups 0 .. e-1.
+//   GATED   h = act(W_gate x + b) (W_up x + b), quantised per 128 features
+//   PLAIN   h = act(W x + b), quantised likewise
+//   LINEAR  y = (W x + b) * roww, bf16
+// With splits > 1 the K blocks of a tile are divided among that many work units, which
+// write fp32 partial sums partial[split][row][column] (pitch floats per row; column
+// 256 n_blk + c is accumulator column c of tile column n_blk) for a reduction kernel.
+struct Fp8GemmArgs {
+  int mode;
+  int E, R, K, N;             // N: features (gated, plain) or outputs (linear)
+  const int32_t* cnt;         // [E], or null: one group of R rows
+  const uint8_t* a;           // [R, K]
+  const float* as;            // [R, ceil(K / 128)]
+  int layout;                 // gated: MOE_GU_CONCAT or MOE_GU_UNFUSED
+  const uint8_t* w;           // [E, N, K]; concat: [E, 2N, K]; unfused: the up rows
+  const float* ws;            // [E, ceil(N / 128), ceil(K / 128)]; concat: [E, 2 ceil(N / 128), ceil(K / 128)]
+  const uint8_t* wg;          // unfused: the gate rows [E, N, K]
+  const float* wgs;
+  const uint16_t* bias;       // bf16, rows as w; or null
+  const uint16_t* gate_bias;  // unfused: [E, N] or null
+  ActParams act;
+  const float* roww;          // linear: [R] or null (1)
+  uint8_t* hq;                // [R, N]
+  float* hs;                  // [R, ceil(N / 128)]
+  uint16_t* y;                // [R, N]
+  int splits;
+  float* partial;
+  int pitch;
+  int max_tiles;              // upper bound of the tile count
+  int num_sms;
+  int* status;
+  int clear_status;           // the kernel starts by clearing *status (a timeout comes seconds later)
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
+
+// N tiles of a GEMM: 256 accumulator columns (128 gated features).
+inline int fp8_n_tiles(int mode, int64_t N) { return (int)((N + (mode == FP8_GATED ? 127 : 255)) / (mode == FP8_GATED ? 128 : 256)); }
+// Upper bound of the row tiles of R rows in E groups: every group adds at most one partial tile.
+inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return R / kFp8BM + (E < R ? E : R); }
+// The split factor of a GEMM (1: none).
+int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms);
+
+// ---------------------------------------------------------------- reductions of split products
+// h of rows 0 .. R-1 from the partial sums of a gated or plain GEMM (same arguments).
+// off [E + 1]: first row of each group (for the biases).
+cudaError_t launch_fp8_reduce_h(const Fp8GemmArgs& a, const int32_t* off, cudaStream_t st);
+// y of a linear GEMM (rows past the groups' sum stay as they were).
+cudaError_t launch_fp8_reduce_y(const Fp8GemmArgs& a, cudaStream_t st);
+// The layer's combine from the partial sums of its down product:
+// y[t] = sum_j w_j (sum_s partial[s][pos[t, j]] + bias) + gate_t Y_shared[t] + shared_output[t]
+struct Fp8CombineArgs {
+  const float* partial;
+  int splits, pitch;
+  const int32_t* pos;         // [T, k]
+  const int32_t* idx;         // [T, k] experts (for the bias)
+  const float* roww;          // [R] or null
+  const uint16_t* bias;       // [E, d] or null
+  const float* sgate;         // [T] or null
+  const uint16_t* Ys;         // [T, d] shared expert rows, or null
+  const uint16_t* shared_output;  // [T, d] or null
+  uint16_t* y;
+  int T, d, k, R, E;
+  int* status;
+};
+cudaError_t launch_fp8_combine(const Fp8CombineArgs& a, cudaStream_t st);
+
+}  // namespace moe
