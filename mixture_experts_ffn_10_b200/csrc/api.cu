@@ -23,6 +23,7 @@
 #include "fp8.cuh"
 #include "moe_ep.h"
 #include "gemv.cuh"
+#include "train.cuh"
 
 namespace moe {
 namespace {
@@ -676,6 +677,8 @@ int forward_on_workspace(const moe_shape* s, const moe_options* o, const moe_ten
 }
 
 int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
+
+int check_layer(const moe_shape* s, const moe_options* o) { return check_shape_opts(s, o); }
 
 int device_sms() { return num_sms_of_current_device(); }
 
