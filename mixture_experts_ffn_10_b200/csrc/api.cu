@@ -410,7 +410,10 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
     fa.N = (int)p.F;
     fa.cnt = sa.cnt;
     fa.a = at<uint8_t>(ws, fp8_base + fr.xq);
+    // scales block by block: neighbouring rows' are read together
     fa.as = at<float>(ws, fp8_base + fr.xs);
+    fa.as_row = 1;
+    fa.as_kb = p.R;
     fa.layout = o->gu_layout;
     fa.w = static_cast<const uint8_t*>(t->gate_up);
     fa.ws = reinterpret_cast<const float*>(t->gate_up_scales);
@@ -421,10 +424,13 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
     fa.act = gc.act;
     fa.hq = at<uint8_t>(ws, fp8_base + fr.hq);
     fa.hs = at<float>(ws, fp8_base + fr.hs);
+    fa.hs_row = 1;
+    fa.hs_grp = p.R;
     fa.splits = p.splits_gu;
     fa.partial = gc.partial;
     fa.pitch = gc.partial_pitch;
-    fa.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fa.mode, p.F));
+    fa.pair = fa.splits == 1 && fp8_pair(p.R, p.E);
+    fa.max_tiles = (int)(fp8_m_tiles(p.R, p.E, fa.pair) * fp8_n_tiles(fa.mode, p.F));
     fa.num_sms = num_sms_of_current_device();
     fa.status = status;
     // the bf16 shared expert: the CTA-pair bf16 kernel over the shared segment alone
@@ -465,14 +471,26 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
     fd.gate_bias = nullptr;
     fd.roww = o->weigh_inputs ? nullptr : sa.roww;
     fd.y = at<uint16_t>(ws, p.o_y);
+    // one expert per token and nothing to add: the expert's row is the token's output
+    const bool direct = p.k == 1 && p.Fs == 0 && !t->shared_output && p.splits_dn == 1;
+    if (direct) {
+      fd.y = static_cast<uint16_t*>(t->y);
+      fd.y_row = sa.perm;
+    }
     fd.splits = p.splits_dn;
-    fd.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fd.mode, p.d));
+    fd.pair = fd.splits == 1 && fp8_pair(p.R, p.E);
+    fd.max_tiles = (int)(fp8_m_tiles(p.R, p.E, fd.pair) * fp8_n_tiles(fd.mode, p.d));
     if ((e = launch_fp8_gemm(fd, st)) != cudaSuccess) return cuda_fail(e, "FP8 down GEMM");
     if (p.Fs > 0) {
       sh.c = shared_gemm(p.nt_dn_shared);
       if ((e = launch_shared_tiles(sh_tiles, (int)p.E, sh.c.max_tiles, st)) != cudaSuccess)
         return cuda_fail(e, "shared tile list");
       if ((e = launch_tc2_down(sh, st)) != cudaSuccess) return cuda_fail(e, "shared expert down GEMM");
+    }
+    if (direct) {
+      for (int i = 5; i <= 6; i++)
+        if ((e = mark(i)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+      return MOE_OK;
     }
     if (fd.splits > 1) {
       if ((e = mark(5)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
@@ -785,6 +803,8 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
   p->rows = p->R + (s->Fs > 0 ? s->T : 0);
   p->Fmax = s->Fs > s->F ? s->Fs : s->F;
   p->nchunks = cdiv(s->T, kChunkTokens);
+  // FP8: few rows sort in one block (77 rows: one launch of 6 us for three of 18)
+  if (s->w_dtype == MOE_FP8 && p->R <= kFp8OneBlockRows) p->nchunks = 1;
   p->act_dtype = s->act_dtype;
   p->w_dtype = s->w_dtype;
   p->logit_dtype = s->logit_dtype;

@@ -10,6 +10,7 @@ namespace moe {
 
 constexpr int kFp8Block = 128;    // columns (and weight rows) that share a scale
 constexpr int kFp8BM = 128;       // rows per tile of the FP8 grouped GEMM (UMMA M)
+constexpr int kFp8OneBlockRows = 512;  // routed rows that one block sorts
 constexpr int kFp8MinNK = 16;     // K (and F) multiple: 16-byte rows
 
 // SMs of the current device.
@@ -58,11 +59,33 @@ __device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
   return t;
 }
 
+// The same for eight values at once, as e4m3 (the first in the low byte).  The quotients
+// x inv round as they are unless one is next to a halfway point: 2^-6 and above those have
+// the low 20 bits 0x80000, below it (steps of 2^-9) they are left to fp8_quotient.
+__device__ __forceinline__ uint2 fp8_round8(const float* x, float s, float inv);
+
 // Four quotients as e4m3, the first in the low byte.
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint2 fp8_round8(const float* x, float s, float inv) {
+  float t[8];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    t[i] = x[i] * inv;
+    const uint32_t u = __float_as_uint(t[i]);
+    near |= ((u - 0x7fff8u) & 0xfffffu) < 16u;               // within 8 units of a halfway point
+    near |= 2u * u - 1u < 2u * __float_as_uint(0x1p-6f) - 1u;  // small, and not zero
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) t[i] = fp8_quotient(x[i], s, inv);
+  }
+  return make_uint2(fp8_pack4(t[0], t[1], t[2], t[3]), fp8_pack4(t[4], t[5], t[6], t[7]));
 }
 
 // ---------------------------------------------------------------- activation
@@ -111,7 +134,7 @@ struct Fp8GatherArgs {
   const int32_t* pos;   // [T, k]
   const float* roww;    // [R]
   uint8_t* xq;          // [R, d]
-  float* xs;            // [R, ceil(d / 128)]
+  float* xs;            // [ceil(d / 128), R]
   int R, d, T, k, weigh_inputs;
   int* status;
 };
@@ -132,7 +155,8 @@ struct Fp8GemmArgs {
   int E, R, K, N;             // N: features (gated, plain) or outputs (linear)
   const int32_t* cnt;         // [E], or null: one group of R rows
   const uint8_t* a;           // [R, K]
-  const float* as;            // [R, ceil(K / 128)]
+  const float* as;            // scale of row r and block b of K at r * as_row + b * as_kb
+  int64_t as_row, as_kb;
   int layout;                 // gated: MOE_GU_CONCAT or MOE_GU_UNFUSED
   const uint8_t* w;           // [E, N, K]; concat: [E, 2N, K]; unfused: the up rows
   const float* ws;            // [E, ceil(N / 128), ceil(K / 128)]; concat: [E, 2 ceil(N / 128), ceil(K / 128)]
@@ -143,11 +167,14 @@ struct Fp8GemmArgs {
   ActParams act;
   const float* roww;          // linear: [R] or null (1)
   uint8_t* hq;                // [R, N]
-  float* hs;                  // [R, ceil(N / 128)]
+  float* hs;                  // scale of row r and group g of h at r * hs_row + g * hs_grp
+  int64_t hs_row, hs_grp;
   uint16_t* y;                // [R, N]
+  const int32_t* y_row;       // linear: row r goes to row y_row[r] of y, or null (row r)
   int splits;
   float* partial;
   int pitch;
+  int pair;                   // CTA pairs: tiles of 256 rows (no splits)
   int max_tiles;              // upper bound of the tile count
   int num_sms;
   int* status;
@@ -158,7 +185,11 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 // N tiles of a GEMM: 256 accumulator columns (128 gated features).
 inline int fp8_n_tiles(int mode, int64_t N) { return (int)((N + (mode == FP8_GATED ? 127 : 255)) / (mode == FP8_GATED ? 128 : 256)); }
 // Upper bound of the row tiles of R rows in E groups: every group adds at most one partial tile.
-inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return R / kFp8BM + (E < R ? E : R); }
+inline int64_t fp8_m_tiles(int64_t R, int64_t E, bool pair = false) {
+  return R / (pair ? 2 * kFp8BM : kFp8BM) + (E < R ? E : R);
+}
+// Whether the GEMMs run on CTA pairs.
+bool fp8_pair(int64_t R, int64_t E);
 // The split factor of a GEMM (1: none).
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms);
 

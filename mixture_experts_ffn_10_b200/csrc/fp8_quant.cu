@@ -47,13 +47,11 @@ __device__ __forceinline__ float lanes_max(float m) {
 
 template <int V>
 __device__ __forceinline__ void store_q(uint8_t* dst, const float (&f)[V], float s, float inv) {
-  uint32_t w[V / 4];
-#pragma unroll
-  for (int i = 0; i < V / 4; i++)
-    w[i] = fp8_pack4(fp8_quotient(f[4 * i], s, inv), fp8_quotient(f[4 * i + 1], s, inv),
-                     fp8_quotient(f[4 * i + 2], s, inv), fp8_quotient(f[4 * i + 3], s, inv));
-  if constexpr (V == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if constexpr (V == 8)
+    *reinterpret_cast<uint2*>(dst) = fp8_round8(f, s, inv);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = fp8_pack4(fp8_quotient(f[0], s, inv), fp8_quotient(f[1], s, inv),
+                                                  fp8_quotient(f[2], s, inv), fp8_quotient(f[3], s, inv));
 }
 
 // Vectorised rows: 128 / V lanes per block, kBatch blocks in flight per group of lanes.
@@ -69,12 +67,18 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const uint8_t* 
   uint4 v[kBatch];
   int64_t row[kBatch];
   int col[kBatch];
+  const int64_t first = b0 / nb;  // one division, then steps of kGroups blocks
+  int down = 0, blk = (int)(b0 - first * nb);
 #pragma unroll
   for (int i = 0; i < kBatch; i++) {
     const int64_t b = b0 + i * kGroups;
-    row[i] = b / nb;
-    const int blk = (int)(b - row[i] * nb);
+    row[i] = first + down;
     col[i] = blk * 128 + lane * V;
+    blk += kGroups;
+    while (blk >= nb) {
+      blk -= nb;
+      down++;
+    }
     v[i] = make_uint4(0, 0, 0, 0);
     if (b < blocks && col[i] < K)
       v[i] = __ldg(reinterpret_cast<const uint4*>(x + row[i] * pitch_bytes + (int64_t)col[i] * (16 / V)));
@@ -191,48 +195,59 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_any_kernel(const vo
 
 // Tokens into expert order: 16 lanes per (token, block of 128 columns), which is read
 // and rounded once and written to the token's k rows (rounded per row for weigh-inputs,
-// whose rows differ by their weight).
+// whose rows differ by their weight); B blocks in flight per group of lanes.
+template <int B>
 __global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs a, int nb) {
   pdl_enter();
-  const int64_t b = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  constexpr int kGroups = kThreads / 16;
+  const int64_t b0 = (int64_t)blockIdx.x * (kGroups * B) + threadIdx.x / 16;
   const int lane = threadIdx.x & 15;
-  const bool live = b < (int64_t)a.T * nb;
-  const int t = live ? (int)(b / nb) : 0;
-  const int blk = live ? (int)(b - (int64_t)t * nb) : 0;
-  const int col = blk * 128 + lane * 8;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (live && col < a.d) v = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d + col));
-  float f[8];
-  unpack16<8>(v, f);
-  const float m = lanes_max<16>(amax_of<8>(f));
-  if (!live) return;
-  float s = fp8_scale(m), inv = __frcp_rn(s);
-  uint2 w;
-  auto round8 = [&](const float (&g)[8]) {
-    w.x = fp8_pack4(fp8_quotient(g[0], s, inv), fp8_quotient(g[1], s, inv), fp8_quotient(g[2], s, inv),
-                    fp8_quotient(g[3], s, inv));
-    w.y = fp8_pack4(fp8_quotient(g[4], s, inv), fp8_quotient(g[5], s, inv), fp8_quotient(g[6], s, inv),
-                    fp8_quotient(g[7], s, inv));
-  };
-  if (!a.weigh_inputs) round8(f);
-  for (int j = 0; j < a.k; j++) {
-    const int row = a.pos[(int64_t)t * a.k + j];
-    if (row < 0 || row >= a.R) {
-      set_status(a.status, MOE_ERR_SHAPE);
-      continue;
-    }
-    if (a.weigh_inputs) {
-      // the largest |w x| is |w| times the largest |x| (rounding is monotone)
-      const float wt = a.roww[row];
-      float g[8];
+  const int first = (int)(b0 / nb);  // one division, then steps of kGroups blocks
+  int blk = (int)(b0 - (int64_t)first * nb), t = first;
+  uint4 v[B];
+  int tok[B], at[B];
 #pragma unroll
-      for (int i = 0; i < 8; i++) g[i] = f[i] * wt;
-      s = fp8_scale(fabsf(m * wt));
-      inv = __frcp_rn(s);
-      round8(g);
+  for (int i = 0; i < B; i++) {
+    tok[i] = t;
+    at[i] = blk;
+    const int col = blk * 128 + lane * 8;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (t < a.T && col < a.d) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d + col));
+    blk += kGroups;
+    while (blk >= nb) {
+      blk -= nb;
+      t++;
     }
-    if (col < a.d) *reinterpret_cast<uint2*>(a.xq + (int64_t)row * a.d + col) = w;
-    if (lane == 0) a.xs[(int64_t)row * nb + blk] = s;
+  }
+#pragma unroll
+  for (int i = 0; i < B; i++) {
+    const int col = at[i] * 128 + lane * 8;
+    float f[8];
+    unpack16<8>(v[i], f);
+    const float m = lanes_max<16>(amax_of<8>(f));
+    if (tok[i] >= a.T) continue;  // (the shuffles are behind: lanes of a group agree, groups need not)
+    float s = fp8_scale(m), inv = __frcp_rn(s);
+    uint2 w = make_uint2(0, 0);
+    if (!a.weigh_inputs) w = fp8_round8(f, s, inv);
+    for (int j = 0; j < a.k; j++) {
+      const int row = a.pos[(int64_t)tok[i] * a.k + j];
+      if (row < 0 || row >= a.R) {
+        set_status(a.status, MOE_ERR_SHAPE);
+        continue;
+      }
+      if (a.weigh_inputs) {
+        // the largest |w x| is |w| times the largest |x| (rounding is monotone)
+        const float wt = a.roww[row];
+        float g[8];
+#pragma unroll
+        for (int c = 0; c < 8; c++) g[c] = f[c] * wt;
+        s = fp8_scale(fabsf(m * wt));
+        inv = __frcp_rn(s);
+        w = fp8_round8(g, s, inv);
+      }
+      if (col < a.d) *reinterpret_cast<uint2*>(a.xq + (int64_t)row * a.d + col) = w;
+      if (lane == 0) a.xs[(int64_t)at[i] * a.R + row] = s;
+    }
   }
 }
 
@@ -278,8 +293,11 @@ cudaError_t launch_shared_tiles(int32_t* tiles, int E, int n, cudaStream_t st) {
 cudaError_t launch_fp8_gather(const Fp8GatherArgs& a, cudaStream_t st) {
   if (a.R == 0) return cudaSuccess;
   const int nb = (a.d + 127) / 128;
-  const int64_t blocks = ((int64_t)a.T * nb + kThreads / 16 - 1) / (kThreads / 16);
-  return launch_pdl(gather_quantize_kernel, (unsigned)blocks, kThreads, 0, st, a, nb);
+  // four blocks in flight once that leaves every SM several thread blocks
+  const int64_t work = (int64_t)a.T * nb, per = kThreads / 16;
+  if (work >= per * 4 * 592)
+    return launch_pdl(gather_quantize_kernel<4>, (unsigned)((work + 4 * per - 1) / (4 * per)), kThreads, 0, st, a, nb);
+  return launch_pdl(gather_quantize_kernel<1>, (unsigned)((work + per - 1) / per), kThreads, 0, st, a, nb);
 }
 
 }  // namespace moe

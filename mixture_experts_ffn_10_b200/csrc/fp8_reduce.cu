@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) reduce_h_kernel(Fp8GemmArgs a, const
     *reinterpret_cast<uint32_t*>(a.hq + (int64_t)row * a.N + f0) =
         fp8_pack4(fp8_quotient(h[0], s, inv), fp8_quotient(h[1], s, inv), fp8_quotient(h[2], s, inv),
                   fp8_quotient(h[3], s, inv));
-  if (lane == 0) a.hs[w] = s;
+  if (lane == 0) a.hs[row * a.hs_row + grp * a.hs_grp] = s;
 }
 
 // Four outputs per thread; the rows of the groups only.

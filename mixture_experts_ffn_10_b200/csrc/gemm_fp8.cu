@@ -3,23 +3,34 @@
 //
 //   acc[r, n] = sum_b xs[r, b] ws[n / 128, b] D_b[r, n],   D_b = sum_{k in block b} xq[r, k] wq[n, k]
 //
-// The tensor cores form D_b exactly as an fp32 accumulation over one block of K (four
-// K = 32 steps) in tensor memory; the scales differ from block to block and row to row,
-// so each D_b is read back and added to an fp32 accumulator with its scale product.  Rows
-// are the MMA's M: a thread of an epilogue warp owns one row and 128 columns of two
-// weight blocks, so a block costs it two scale products and 128 multiply-adds (64
-// packed ones), and the accumulators live in its registers for the whole K loop.
-// (With the weights as M the row scales would differ from register to register and each
-// multiply-add would need an operand from shared memory.)  Two 256-column halves of
-// tensor memory alternate: while block b is added up, block b + 1 is multiplied.
+// The tensor cores form D_b as an fp32 accumulation over one block of K (four K = 32
+// steps) in tensor memory; the scales differ from block to block and row to row, so each
+// D_b is read back and added to an fp32 accumulator with its scale product.  Rows are the
+// MMA's M: a thread of an epilogue warp owns one row and 64 columns of each of the tile's
+// two weight blocks, so a block of K costs it two scale products and 128 multiply-adds,
+// and the accumulators live in its registers for the whole K loop.  (With the weights as M
+// the row scales would differ from register to register and each multiply-add would need
+// an operand from shared memory.)  Tensor memory is a ring of four quarters of 128 columns;
+// a block of K is two MMA groups of N = 128 (64 rows of each weight block), each handed
+// over by itself, so that the adds of one quarter run beside the products of the others:
+// with two halves of 256 columns the chain product - hand-over - adds - hand-over of a
+// buffer was longer than two products.
 //
-// Work: tiles of 128 rows x 256 weight rows (128 gate and their 128 up rows, or 256 plain
-// rows), persistent CTAs, one per SM; the tile list is made on the device from the
-// groups' row counts.  Warps: 0 TMA producer (128 x 128 and 256 x 128 bytes per stage,
-// 128-byte swizzle), 1 TMEM and MMA issue, 4-11 epilogue (TMEM lane quadrant x column
-// half).  The epilogue's 128 accumulators a thread do not fit the 168 registers that
-// twelve warps leave each: the first four warps hand theirs over (setmaxnreg, 56 + 2 x
-// 224 = 3 x 168).  Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.
+// Work: tiles of 256 weight rows (128 gate and their 128 up rows, or 256 plain rows) by
+// 128 rows on one CTA, or by 256 rows on a CTA pair (cta_group::2, each CTA staging its
+// 128 rows and half of the weights); persistent CTAs, one per SM; the tile list is made on
+// the device from the groups' row counts.  Warps of a CTA:
+//   0     TMA producer (128-byte swizzle, one block of K per stage);
+//   1, 3  MMA issue (of a pair: in the even CTA), blocks of K in turn; 1: TMEM, too;
+//   2     the products of row and weight scales, a ring of blocks ahead in shared memory
+//         (read by the epilogue itself they cost it a memory latency per block);
+//   4-11  epilogue: TMEM lane quadrant x column half.  Their accumulators do not fit the
+//         168 registers that twelve warps leave each: the first four warps hand theirs
+//         over (setmaxnreg, 4 x 88 + 8 x 208 = 12 x 168).
+// Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.
+#include <atomic>
+#include <cstdlib>
+
 #include "fp8.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -32,77 +43,163 @@ using namespace sm100;
 constexpr int BM = kFp8BM;
 constexpr int BK = kFp8Block;     // bytes of K per stage: one scale block
 constexpr int BNB = 256;          // weight rows per tile
-constexpr int B_BYTES = BNB * BK;
-constexpr int ACC_COLS = BNB;
-constexpr int TMEM_COLS = 2 * ACC_COLS;
+constexpr int BNH = 128;          // of them per MMA group: 64 of each of the tile's two weight blocks
+constexpr int kQuarters = 4;      // accumulators of BNH columns in tensor memory
+constexpr int TMEM_COLS = kQuarters * BNH;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
-constexpr int kControlRegs = 56, kEpiRegs = 224;  // of 168 at launch: 4 x 56 + 8 x 224 = 12 x 168
+constexpr int kControlRegs = 88, kEpiRegs = 208;  // of 168 at launch: 4 x 88 + 8 x 208 = 12 x 168
 constexpr int kMaxStages = 6;
+constexpr int kScaleBatch = 8;    // blocks of K whose scale products are handed over together
+constexpr int kScaleSlots = 2 * kScaleBatch;
 constexpr int kSmemLimit = 232448;
 // kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B e4m3 (format 0), K-major, N >> 3
-// in bits 17-22, M >> 4 in 24-28.
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BNB >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+// in bits 17-22, M >> 4 in 24-28 (M = 128, or 256 over a pair).
+constexpr uint32_t idesc(bool pair) {
+  return (1u << 4) | ((uint32_t)(BNH >> 3) << 17) | ((uint32_t)((pair ? 2 * BM : BM) >> 4) << 24);
+}
+constexpr uint16_t kBothCtas = 0x3, kEvenCta = 0x1;
 
-// Shared memory after the stages: barriers, the row maxima the two column halves of a
-// tile exchange, the groups' first rows and tile prefixes.
-struct Meta {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+// Shared memory after the stages: scale products, barriers, the row maxima the two column
+// halves of a tile exchange, the groups' first rows and tile prefixes.  The quarters'
+// barriers are aligned so that quarters 0, 1 and 2, 3 differ by one address bit.
+struct alignas(64) Meta {
+  float2 scale[kScaleSlots][BM];  // [block of K mod slots][row]: times the two weight blocks' scales
+  float amax[2][2][BM];           // [group of 128 columns][column half][row]
+  uint64_t tfull[kQuarters], tempty[kQuarters];
+  uint64_t full[kMaxStages], empty[kMaxStages], sfull[2], sempty[2], drain;
   uint32_t tmem_slot;
   int abort_flag;
-  float amax[2][2][BM];  // [group of 128 columns][column half][row]
 };
 
-constexpr int stage_bytes(int abox) { return abox * BK + B_BYTES; }
+constexpr int stage_bytes(int abox, bool pair) { return (abox + (pair ? BNB / 2 : BNB)) * BK; }
 constexpr int meta_bytes(int E) { return (int)sizeof(Meta) + 2 * (E + 1) * 4; }
-constexpr int stages_for(int abox, int E) {
-  const int n = (kSmemLimit - 1024 - meta_bytes(E)) / stage_bytes(abox);
+constexpr int stages_for(int abox, bool pair, int E) {
+  const int n = (kSmemLimit - 1024 - meta_bytes(E)) / stage_bytes(abox, pair);
   return n > kMaxStages ? kMaxStages : n;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc(true)), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc(false)), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued before have completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR) mma_commit_pair(bar, kBothCtas);
+  else mma_commit(bar);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// Waits for the thread's TMEM loads; r is in place after it (and not read before).
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
-// acc (two floats) += {a, b} * f (two floats)
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t a, uint32_t b, uint64_t f) {
-  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(a), "r"(b), "l"(f));
+// True in one lane of a converged warp.  The compiler knows that the branch on it runs in
+// one thread: issuing MMAs and commits there takes a third of the cycles that a branch on
+// the lane number takes (4 MMAs and 2 commits: about 200 cycles instead of 450).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
-__device__ __forceinline__ uint64_t twice(float f) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
-  return r;
-}
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // The two column halves (warps w and w + 4) of a TMEM lane quadrant meet.
 __device__ __forceinline__ void quadrant_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory"); }
+
+// The same value in every lane, in a form that the compiler knows to be uniform: loops and
+// branches on it need no reconvergence around the whole-warp tensor memory loads (with
+// bounds read from shared memory by every lane, those cost the K loop much of its time).
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Barriers by shared-memory address: a loop keeps one register per role, not a pointer per
+// barrier.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {  // suspends for some microseconds at most
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {  // does not suspend
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The rest of a wait whose first attempt was in vain: until the phase completes, another
+// role gives up (*abort) or 2 s have passed.
+__device__ __forceinline__ bool keep_waiting(uint32_t bar, uint32_t parity, uint32_t abort, int* status) {
+  const uint64_t t0 = global_timer();
+  while (!try_wait(bar, parity)) {
+    int stop;
+    asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
+    if (stop) return false;
+    if (global_timer() - t0 > kTimeoutNs) {
+      asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+      set_status(status, MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t abort, int* status) {  // one thread
+  return try_wait(bar, parity) || keep_waiting(bar, parity, abort, status);
+}
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, uint32_t abort, int* status) {
+  if (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
+    keep_waiting(bar, parity, abort, status);
+    __syncwarp();
+  }
+}
+// One lane arrives, without a branch.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(lane)
+      : "memory");
+}
+// The same on a barrier of either CTA of a pair, to hand over tensor memory only (read to
+// registers, fenced).  With release semantics it would wait for the thread's other memory
+// operations, and the epilogue makes one per quarter.
+__device__ __forceinline__ void warp_arrive_cluster_relaxed(uint32_t bar_cluster, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar_cluster),
+      "r"(lane)
+      : "memory");
+}
 
 struct Unit {
   int e, m0, n_blk, rows, row0, sp, kb0, kb1;
 };
 
 // Unit u of the list: split-fastest, then row tile, then N block, then group.
+template <int BMT>  // rows per tile
 __device__ __forceinline__ Unit unit_of(const Fp8GemmArgs& p, const int32_t* row0, const int32_t* tiles, int u, int nkb) {
   Unit r;
   const int tile = u / p.splits;
@@ -116,20 +213,93 @@ __device__ __forceinline__ Unit unit_of(const Fp8GemmArgs& p, const int32_t* row
   r.e = lo;
   r.row0 = row0[lo];
   r.rows = row0[lo + 1] - r.row0;
-  const int mt = (r.rows + BM - 1) / BM;
+  const int mt = (r.rows + BMT - 1) / BMT;
   const int local = tile - tiles[lo];
   r.n_blk = local / mt;
-  r.m0 = (local % mt) * BM;
+  r.m0 = (local % mt) * BMT;
   r.kb0 = r.sp * nkb / p.splits;
   r.kb1 = (r.sp + 1) * nkb / p.splits;
   return r;
 }
 
-template <int MODE, int ABOX>
+// Scale rows of a tile's two weight blocks: [ceil(K / 128)] each.
+struct BlockScales {
+  const float *w0, *w1;
+};
+template <int MODE>
+__device__ __forceinline__ BlockScales block_scales(const Fp8GemmArgs& p, const Unit& t, int nbn, int nkb) {
+  BlockScales b;
+  if (MODE == FP8_GATED) {
+    const bool cat = p.layout != MOE_GU_UNFUSED;
+    b.w0 = cat ? p.ws + ((int64_t)t.e * 2 * nbn + t.n_blk) * nkb : p.wgs + ((int64_t)t.e * nbn + t.n_blk) * nkb;
+    b.w1 = cat ? b.w0 + (int64_t)nbn * nkb : p.ws + ((int64_t)t.e * nbn + t.n_blk) * nkb;
+  } else {
+    b.w0 = p.ws + ((int64_t)t.e * nbn + 2 * t.n_blk) * nkb;
+    b.w1 = 2 * t.n_blk + 1 < nbn ? b.w0 + nkb : b.w0;
+  }
+  return b;
+}
+
+// Features f0 .. f0 + 31 of a row: gate (or plain) sums in g, up sums in u -> activated
+// values in g; returns their largest magnitude.  One activation per instance, so that the
+// 32 unrolled values run a short straight piece of code.
+template <bool GATED, int ACT>
+__device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], const ActParams& act, int f0, int N) {
+  ActParams a = act;
+  a.act = ACT;
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i++) {
+    float h = fp8_act(a, g[i], GATED);
+    if (GATED) h *= fp8_up(a, u[i]) + a.beta;
+    g[i] = f0 + i < N ? h : 0.f;
+    m = fmaxf(m, fabsf(g[i]));
+  }
+  return m;
+}
+template <bool GATED>
+__device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], const ActParams& act, int f0, int N) {
+  switch (act.act) {
+    case MOE_ACT_SILU: return activate<GATED, MOE_ACT_SILU>(g, u, act, f0, N);
+    case MOE_ACT_GELU_ERF: return activate<GATED, MOE_ACT_GELU_ERF>(g, u, act, f0, N);
+    case MOE_ACT_GELU_TANH: return activate<GATED, MOE_ACT_GELU_TANH>(g, u, act, f0, N);
+    case MOE_ACT_RELU: return activate<GATED, MOE_ACT_RELU>(g, u, act, f0, N);
+    default: return activate<GATED, MOE_ACT_IDENTITY>(g, u, act, f0, N);
+  }
+}
+
+// v[i] += bias[c0 + i] for the columns below N (a multiple of 8).
+__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t* bias, int c0, int N) {
+  const bool vec = (reinterpret_cast<uintptr_t>(bias + c0) & 15u) == 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (c0 + i < N) {
+      uint4 q;
+      if (vec) {
+        q = __ldg(reinterpret_cast<const uint4*>(bias + c0 + i));
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+          w[c] = __ldg(bias + c0 + i + 2 * c) | ((uint32_t)__ldg(bias + c0 + i + 2 * c + 1) << 16);
+        q = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        v[i + 2 * c] += bf16_to_f32(w[c] & 0xffff);
+        v[i + 2 * c + 1] += bf16_to_f32(w[c] >> 16);
+      }
+    }
+  }
+}
+
+template <int MODE, int ABOX, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmG, const Fp8GemmArgs p, const int stages) {
-  constexpr int STAGE_BYTES = stage_bytes(ABOX), A_BYTES = ABOX * BK;
+  constexpr int STAGE_BYTES = stage_bytes(ABOX, PAIR), A_BYTES = ABOX * BK;
+  constexpr int BMT = PAIR ? 2 * BM : BM;   // rows per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta& meta = *reinterpret_cast<Meta*>(smem + stages * STAGE_BYTES);
@@ -137,17 +307,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* tiles = row0 + p.E + 1;                         // [E + 1]
   volatile int* abort_flag = &meta.abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;  // 0 issues the MMAs
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; s++) {
       mbar_init(&meta.full[s], 1);
       mbar_init(&meta.empty[s], 1);
     }
-    for (int b = 0; b < 2; b++) {
+    for (int b = 0; b < kQuarters; b++) {
       mbar_init(&meta.tfull[b], 1);
-      mbar_init(&meta.tempty[b], kEpiWarps);
+      mbar_init(&meta.tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
     }
-    mbar_init(&meta.drain, 1);
+    for (int s = 0; s < 2; s++) {
+      mbar_init(&meta.sfull[s], 1);
+      mbar_init(&meta.sempty[s], kEpiWarps);
+    }
+    mbar_init(&meta.drain, 2);  // both MMA issuers
     meta.abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tmA);
@@ -155,14 +331,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED) prefetch_tmap(&tmG);
   }
   if (warp == 1) {
-    tmem_alloc(&meta.tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&meta.tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&meta.tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   pdl_enter();
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
   for (int e = threadIdx.x; e < p.E; e += kThreads) row0[e] = p.cnt ? p.cnt[e] : p.R;
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();  // barriers and TMEM of both CTAs
+  else __syncthreads();
   tc_fence_after();
   const int nt = (p.N + (MODE == FP8_GATED ? 127 : 255)) / (MODE == FP8_GATED ? 128 : 256);
   if (warp == 2) {
@@ -180,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int32_t first = (int32_t)min(rows_before + incl - c, (int64_t)p.R);
       const int32_t end = (int32_t)min(rows_before + incl, (int64_t)p.R);
-      const int32_t mt = (end - first + BM - 1) / BM * nt;
+      const int32_t mt = (end - first + BMT - 1) / BMT * nt;
       int32_t tincl = mt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,37 +383,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const uint32_t tmem_base = meta.tmem_slot;
-  const int nkb = (p.K + BK - 1) / BK;
-  const int total = tiles[p.E] * p.splits;
+  // Addresses in shared memory; what every role needs is formed again where it is used
+  // (kept across the roles it would be spilled).
+  const uint32_t abort = smem_u32(&meta.abort_flag);
 
   if (warp < kFirstEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       // ---------------------------------------------------------- TMA producer
+      const int nkb = (p.K + BK - 1) / BK, total = tiles[p.E] * p.splits;
+      const uint32_t full = smem_u32(meta.full), empty = smem_u32(meta.empty);
       int s = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit t = unit_of(p, row0, tiles, u, nkb);
+      for (int u = worker; ok && u < total; u += workers) {
+        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+        const int arow = t.row0 + t.m0 + BM * rank;
         for (int kb = t.kb0; kb < t.kb1; kb++) {
-          if (!mbar_wait(&meta.empty[s], phase ^ 1, abort_flag, p.status)) {
+          if (!wait(empty + 8 * s, phase ^ 1, abort, p.status)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&meta.full[s], STAGE_BYTES);
           uint8_t* sa = smem + s * STAGE_BYTES;
           uint8_t* sb = sa + A_BYTES;
           const int k0 = kb * BK;
-          tma_load_2d(&tmA, &meta.full[s], sa, k0, t.row0 + t.m0);
-          if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED) {
-            tma_load_3d(&tmG, &meta.full[s], sb, k0, t.n_blk * 128, t.e);
-            tma_load_3d(&tmB, &meta.full[s], sb + B_BYTES / 2, k0, t.n_blk * 128, t.e);
-          } else if (MODE == FP8_GATED) {  // [E][2][N][K]: gate rows, then up rows
-            tma_load_4d(&tmB, &meta.full[s], sb, k0, t.n_blk * 128, 0, t.e);
-            tma_load_4d(&tmB, &meta.full[s], sb + B_BYTES / 2, k0, t.n_blk * 128, 1, t.e);
+          if constexpr (PAIR) {
+            // The even CTA arms its stage for the bytes of both; the odd CTA's may land
+            // first (the phase cannot complete before the arrival).
+            const uint32_t fb = mapa_shared(&meta.full[s], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&meta.full[s], 2 * STAGE_BYTES);
+            tma_load_2d_pair(&tmA, fb, sa, k0, arow);
+            // the even CTA stages the first weight block (gate rows), the odd one the second
+            // (up): an MMA group takes 64 rows from each
+            if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
+              tma_load_3d_pair(rank == 0 ? &tmG : &tmB, fb, sb, k0, t.n_blk * 128, t.e);
+            else if (MODE == FP8_GATED)
+              tma_load_4d_pair(&tmB, fb, sb, k0, t.n_blk * 128, rank, t.e);
+            else
+              tma_load_3d_pair(&tmB, fb, sb, k0, t.n_blk * BNB + 128 * rank, t.e);
           } else {
-            tma_load_3d(&tmB, &meta.full[s], sb, k0, t.n_blk * BNB, t.e);
+            mbar_arrive_expect_tx(&meta.full[s], STAGE_BYTES);
+            tma_load_2d(&tmA, &meta.full[s], sa, k0, arow);
+            // rows in MMA order: 64 of the first weight block (gate), 64 of the second (up), ...
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const int blk = g & 1, r = (g >> 1) * 64;
+              uint8_t* dst = sb + g * 64 * BK;
+              if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
+                tma_load_3d(blk ? &tmB : &tmG, &meta.full[s], dst, k0, t.n_blk * 128 + r, t.e);
+              else if (MODE == FP8_GATED)  // [E][2][N][K]
+                tma_load_4d(&tmB, &meta.full[s], dst, k0, t.n_blk * 128 + r, blk, t.e);
+              else
+                tma_load_3d(&tmB, &meta.full[s], dst, k0, t.n_blk * BNB + blk * 128 + r, t.e);
+            }
           }
           issued++;
           if (++s == stages) {
@@ -240,117 +444,246 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every load issued has landed before the CTA may exit: the last `stages` of them
+      // every load issued has landed before the CTA may exit (the last `stages` of them);
+      // of a pair: has been consumed, which both CTAs' empty barriers see
       const uint32_t n = issued < (uint32_t)stages ? issued : (uint32_t)stages;
+      const uint32_t landed = PAIR ? empty : full;
       for (uint32_t j = issued - n; j < issued; j++) {
         const uint64_t t0 = global_timer();
-        while (!mbar_try_wait(&meta.full[j % stages], (j / stages) & 1) && global_timer() - t0 < kTimeoutNs) {
+        while (!try_wait(landed + 8 * (j % stages), (j / stages) & 1) && global_timer() - t0 < kTimeoutNs) {
         }
       }
-    } else if (warp == 1 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      int s = 0;
-      uint32_t phase = 0, it = 0;
+    } else if ((warp == 1 || warp == 3) && rank == 0 && elect_one()) {
+      // ---------------------------------------------------------- MMA issuers
+      // Warp 1 takes the even blocks of K (quarters 0, 1), warp 3 the odd ones (2, 3): a
+      // barrier answers after some hundred cycles on a busy SM, and one thread's waits for a
+      // stage and two quarters took longer than the block's products.
+      const int nkb = (p.K + BK - 1) / BK, total = tiles[p.E] * p.splits;
+      const uint32_t odd = warp >> 1, q0 = 2 * odd;
+      const uint32_t full = smem_u32(meta.full), tempty = smem_u32(meta.tempty) + 8 * q0;
+      const uint32_t tmem_base = meta.tmem_slot + q0 * BNH;
+      const uint64_t ad0 = sdesc_k_sw128(smem_u32(smem)), bd0 = sdesc_k_sw128(smem_u32(smem) + A_BYTES);
+      int s = odd;
+      uint32_t phase = 0, par = 1, n = 0;  // n: blocks of K so far
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit t = unit_of(p, row0, tiles, u, nkb);
-        for (int kb = t.kb0; kb < t.kb1; kb++, it++) {
-          const int acc = it & 1;
-          if (!mbar_wait(&meta.tempty[acc], ((it >> 1) & 1) ^ 1, abort_flag, p.status) ||
-              !mbar_wait(&meta.full[s], phase, abort_flag, p.status)) {
+      for (int u = worker; ok && u < total; u += workers) {
+        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+        const int len = t.kb1 - t.kb0;
+        for (int i = (n ^ odd) & 1; i < len; i += 2) {
+          // all three are asked before the first answer is awaited
+          const bool loaded = test_wait(full + 8 * s, phase), free0 = test_wait(tempty, par), free1 = test_wait(tempty + 8, par);
+          if (!(loaded || wait(full + 8 * s, phase, abort, p.status)) || !(free0 || wait(tempty, par, abort, p.status))) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
-          const uint64_t ad = sdesc_k_sw128(sa), bd = sdesc_k_sw128(sa + A_BYTES);
+          const uint64_t ad = ad0 + s * (STAGE_BYTES / 16), bd = bd0 + s * (STAGE_BYTES / 16);
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; kk++) mma_f8(tmem_base + acc * ACC_COLS, ad + 2 * kk, bd + 2 * kk, kk > 0);
-          mma_commit(&meta.empty[s]);
-          mma_commit(&meta.tfull[acc]);
-          if (++s == stages) {
-            s = 0;
+          for (int h = 0; h < 2; h++) {
+            if (h == 1 && !(free1 || wait(tempty + 8, par, abort, p.status))) {
+              ok = false;
+              break;
+            }
+            // (the epilogue warps, of a pair the odd CTA's too, hand over tensor memory only,
+            // for which this fence is the acquire)
+            tc_fence_after();
+            // rows 128 h .. of the stage's weights (of a pair: 64 h .. in each CTA)
+            const uint64_t bh = bd + (h * (PAIR ? 64 : 128) * BK) / 16;
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; kk++) mma_f8<PAIR>(tmem_base + h * BNH, ad + 2 * kk, bh + 2 * kk, kk > 0);
+            commit<PAIR>(&meta.tfull[q0 + h]);
+          }
+          if (!ok) break;
+          commit<PAIR>(&meta.empty[s]);
+          par ^= 1;
+          if ((s += 2) >= stages) {
+            s -= stages;
             phase ^= 1;
           }
         }
+        n += len;
       }
       // all issued MMAs complete before the tensor memory is released
-      mma_commit(&meta.drain);
+      if (PAIR) mma_commit_pair(&meta.drain, kEvenCta);
+      else mma_commit(&meta.drain);
       const uint64_t t0 = global_timer();
       while (!mbar_try_wait(&meta.drain, 0) && global_timer() - t0 < kTimeoutNs) {
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- scale products
+      constexpr int kLoad = 4;  // blocks of K whose scales are loaded together, of four rows per lane
+      const int nkb = (p.K + BK - 1) / BK, nbn = (p.N + 127) / 128, total = uniform(tiles[p.E] * p.splits);
+      const uint32_t sfull = smem_u32(meta.sfull), sempty = smem_u32(meta.sempty);
+      const bool vec = p.as_kb == 1 && p.as_row % 4 == 0 && (reinterpret_cast<uintptr_t>(p.as) & 15u) == 0;
+      uint32_t n = 0;  // blocks of K so far
+      bool ok = true;
+      for (int u = worker; ok && u < total; u += workers) {
+        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+        const BlockScales w = block_scales<MODE>(p, t, nbn, nkb);
+        const int m0 = t.m0 + BM * rank + lane, kb1 = uniform(t.kb1);
+        const float* x[4];  // rows past the last: any
+#pragma unroll
+        for (int r = 0; r < 4; r++) x[r] = p.as + (int64_t)(t.row0 + min(m0 + 32 * r, t.rows - 1)) * p.as_row;
+        for (int kb = uniform(t.kb0); ok && kb < kb1; kb += kLoad) {
+          float xs[4][kLoad], wa[kLoad], wb[kLoad];
+#pragma unroll
+          for (int i = 0; i < kLoad; i++) {
+            const int k = min(kb + i, kb1 - 1);
+            wa[i] = __ldg(w.w0 + k);
+            wb[i] = __ldg(w.w1 + k);
+          }
+          if (vec && kb % 4 == 0 && kb + kLoad <= kb1) {
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const float4 a = __ldg(reinterpret_cast<const float4*>(x[r] + kb));
+              xs[r][0] = a.x, xs[r][1] = a.y, xs[r][2] = a.z, xs[r][3] = a.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kLoad; i++) {
+              const int64_t k = (int64_t)min(kb + i, kb1 - 1) * p.as_kb;
+#pragma unroll
+              for (int r = 0; r < 4; r++) xs[r][i] = __ldg(x[r] + k);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kLoad; i++) {
+            if (kb + i < kb1) {
+              const uint32_t g = (n / kScaleBatch) & 1;  // half of the ring
+              if (n % kScaleBatch == 0) warp_wait(sempty + 8 * g, ((n / kScaleSlots) & 1) ^ 1, abort, p.status);
+#pragma unroll
+              for (int r = 0; r < 4; r++)
+                meta.scale[n % kScaleSlots][lane + 32 * r] = make_float2(xs[r][i] * wa[i], xs[r][i] * wb[i]);
+              if (++n % kScaleBatch == 0) {
+                __syncwarp();
+                warp_arrive(sfull + 8 * g, lane);
+              }
+            }
+          }
+          ok = __all_sync(0xffffffffu, *abort_flag == 0);
+        }
+      }
+      if (n % kScaleBatch != 0) {  // the last blocks
+        __syncwarp();
+        warp_arrive(sfull + 8 * ((n / kScaleBatch) & 1), lane);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ------------------------------------------------------------ epilogue
+    const int nkb = (p.K + BK - 1) / BK, nbn = (p.N + 127) / 128, units = uniform(tiles[p.E] * p.splits);
     const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
-    const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + half * 64;
-    const int nbn = (p.N + 127) / 128;
-    uint32_t it = 0;
+    const int r_in_tile = q * 32 + lane;  // of the CTA's 128 rows
+    // The current block's quarters: columns half * 32 .. + 31 of the 64 of each weight block,
+    // and their barriers; quarters 0, 1 and 2, 3 take turns by one address bit.
+    uint32_t tq = meta.tmem_slot + ((uint32_t)(q * 32) << 16) + half * 32;
+    uint32_t fq = smem_u32(meta.tfull), eq = PAIR ? mapa_shared(meta.tempty, 0) : smem_u32(meta.tempty);
+    const uint32_t sfull = smem_u32(meta.sfull), sempty = smem_u32(meta.sempty);
+    const uint32_t srow = smem_u32(meta.scale) + r_in_tile * 8;
+    uint32_t n = 0, sn = 0;  // blocks of K so far, and whose scales were read
+    auto drained = [&](uint32_t bar) {
+      if (PAIR) warp_arrive_cluster_relaxed(bar, lane);
+      else warp_arrive(bar, lane);
+    };
+    // this row's two scale products of the next block (each block once, in order)
+    auto next_scales = [&]() -> float2 {
+      float2 f;
+      const uint32_t g = 8 * ((sn / kScaleBatch) & 1);
+      if (sn % kScaleBatch == 0) warp_wait(sfull + g, (sn / kScaleSlots) & 1, abort, p.status);
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(f.x), "=f"(f.y)
+                   : "r"(srow + (sn % kScaleSlots) * (BM * 8))
+                   : "memory");
+      if (++sn % kScaleBatch == 0) {
+        __syncwarp();
+        warp_arrive(sempty + g, lane);
+      }
+      return f;
+    };
     // A wait that gives up does not leave the loop: both halves of a quadrant meet in
     // every unit, so they walk the same list to its end (the waits then return at once).
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      const Unit t = unit_of(p, row0, tiles, u, nkb);
-      const int r_in_tile = q * 32 + lane;
-      const bool valid = t.m0 + r_in_tile < t.rows;
-      const int64_t grow = (int64_t)t.row0 + t.m0 + r_in_tile;
-      const bool live = t.m0 + q * 32 < t.rows;  // whole warp: some row of this quadrant exists
-      // scales: this row's, and those of the tile's two weight blocks
-      const float* as = p.as + (valid ? grow : (int64_t)t.row0) * nkb;
-      const float *w0, *w1;
-      if (MODE == FP8_GATED) {
-        const bool cat = p.layout != MOE_GU_UNFUSED;
-        w0 = cat ? p.ws + ((int64_t)t.e * 2 * nbn + t.n_blk) * nkb : p.wgs + ((int64_t)t.e * nbn + t.n_blk) * nkb;
-        w1 = cat ? w0 + (int64_t)nbn * nkb : p.ws + ((int64_t)t.e * nbn + t.n_blk) * nkb;
-      } else {
-        w0 = p.ws + ((int64_t)t.e * nbn + 2 * t.n_blk) * nkb;
-        w1 = 2 * t.n_blk + 1 < nbn ? w0 + nkb : w0;
-      }
-      uint64_t acc[2][32];  // two sets of 64 columns: half * 64 .. of each weight block
+    for (int u = worker; u < units; u += workers) {
+      const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+      const int kb0 = uniform(t.kb0), kb1 = uniform(t.kb1);
+      const int m = uniform(t.m0) + BM * rank;
+      const bool valid = m + r_in_tile < t.rows;
+      const int64_t grow = (int64_t)t.row0 + m + r_in_tile;
+      const bool live = m + q * 32 < uniform(t.rows);  // whole warp: some row of this quadrant exists
+      // Sums by weight block: acc[b][32 h + i] is row 64 h + 32 half + i of block b.
+      float acc[2][64];
 #pragma unroll
-      for (int i = 0; i < 32; i++) acc[0][i] = acc[1][i] = 0;
-      float xs = 0.f, s0 = 0.f, s1 = 0.f;
-      if (live && t.kb0 < t.kb1) {
-        xs = __ldg(as + t.kb0);
-        s0 = __ldg(w0 + t.kb0);
-        s1 = __ldg(w1 + t.kb0);
-      }
-      for (int kb = t.kb0; kb < t.kb1; kb++, it++) {
-        const int buf = it & 1;
-        const uint64_t f[2] = {twice(xs * s0), twice(xs * s1)};
-        if (live && kb + 1 < t.kb1) {
-          xs = __ldg(as + kb + 1);
-          s0 = __ldg(w0 + kb + 1);
-          s1 = __ldg(w1 + kb + 1);
-        }
-        mbar_wait(&meta.tfull[buf], (it >> 1) & 1, abort_flag, p.status);
-        __syncwarp();
-        tc_fence_after();
-        if (live) {
+      for (int i = 0; i < 64; i++) acc[0][i] = acc[1][i] = 0.f;
+      if (!live) {
+        for (int kb = kb0; kb < kb1; kb++, n++) {
+          next_scales();
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            uint32_t v[32];
-            tmem_ld32(tb + buf * ACC_COLS + (c >> 1) * 128 + (c & 1) * 32, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i++) fma2(acc[c >> 1][(c & 1) * 16 + i], v[2 * i], v[2 * i + 1], f[c >> 1]);
+          for (int h = 0; h < 2; h++) {
+            warp_wait(fq + 8 * h, (n >> 1) & 1, abort, p.status);
+            drained(eq + 8 * h);
           }
+          tq ^= 2 * BNH;
+          fq ^= 16;
+          eq ^= 16;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&meta.tempty[buf]);
+      } else if (kb0 < kb1) {
+        // One run of 16 columns after another through all quarters: while 16 columns are
+        // added the next 16 are on their way, the next quarter's first ones too, and whether
+        // that quarter is ready is asked before the adds in between (the answer takes some
+        // hundred cycles on a busy SM).
+        uint32_t v[2][16];
+        float2 next = next_scales();
+        warp_wait(fq, (n >> 1) & 1, abort, p.status);
+        tc_fence_after();
+        tmem_ld16(tq, v[0]);
+        for (int left = kb1 - kb0; left > 0; left--, n++) {
+          const float f[2] = {next.x, next.y};
+          if (left > 1) next = next_scales();
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const bool asked = h == 0 || left > 1;
+            const uint32_t nf = h == 0 ? fq + 8 : fq ^ 16, npar = ((n + h) >> 1) & 1;
+            const uint32_t nt = h == 0 ? tq + BNH : tq ^ (2 * BNH);
+            bool ready = true;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {  // weight block c / 2, columns 16 (c % 2) ..
+              tmem_ld_wait16(v[c & 1]);
+              if (c < 3) {
+                tmem_ld16(tq + h * BNH + ((c + 1) >> 1) * 64 + ((c + 1) & 1) * 16, v[(c + 1) & 1]);
+                if (c == 1 && asked) ready = test_wait(nf, npar);
+              } else {
+                tc_fence_before();
+                drained(eq + 8 * h);
+                if (asked && !__all_sync(0xffffffffu, ready)) warp_wait(nf, npar, abort, p.status);
+                tc_fence_after();
+                tmem_ld16(nt, v[0]);  // (after the last quarter: whatever the next holds, not used)
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i++) {
+                float& a = acc[c >> 1][h * 32 + (c & 1) * 16 + i];
+                a = fmaf(__uint_as_float(v[c & 1][i]), f[c >> 1], a);
+              }
+            }
+          }
+          tq ^= 2 * BNH;
+          fq ^= 16;
+          eq ^= 16;
+        }
+        tmem_ld_wait16(v[0]);
       }
 
+      // acc[b][32 h ..] starts at row (column of the output) row_of(h) of weight block b
+      auto row_of = [&](int h) { return h * 64 + half * 32; };
       if (p.splits > 1) {
         if (valid) {
 #pragma unroll
-          for (int j = 0; j < 2; j++) {
-            float4* out = reinterpret_cast<float4*>(p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB +
-                                                    j * 128 + half * 64);
+          for (int b = 0; b < 2; b++) {
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-              out[i] = make_float4(lo_of(acc[j][2 * i]), hi_of(acc[j][2 * i]), lo_of(acc[j][2 * i + 1]),
-                                   hi_of(acc[j][2 * i + 1]));
+            for (int h = 0; h < 2; h++) {
+              float4* out = reinterpret_cast<float4*>(p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB +
+                                                      b * 128 + row_of(h));
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                out[i / 4] = make_float4(acc[b][h * 32 + i], acc[b][h * 32 + i + 1], acc[b][h * 32 + i + 2], acc[b][h * 32 + i + 3]);
+            }
           }
         }
         continue;
@@ -358,74 +691,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (MODE == FP8_LINEAR) {
         if (valid) {
           const float w = p.roww ? p.roww[grow] : 1.f;
+          const int64_t orow = p.y_row ? p.y_row[grow] : grow;
 #pragma unroll
-          for (int j = 0; j < 2; j++) {
-            const int n0 = t.n_blk * BNB + j * 128 + half * 64;
-            const uint16_t* bias = p.bias ? p.bias + (int64_t)t.e * p.N : nullptr;
-            uint16_t* out = p.y + grow * p.N;
+          for (int b = 0; b < 2; b++) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              if (n0 + 8 * i >= p.N) break;  // N is a multiple of 8
-              float b[8];
+            for (int h = 0; h < 2; h++) {
+              float (&v)[32] = *reinterpret_cast<float (*)[32]>(&acc[b][h * 32]);
+              const int n0 = t.n_blk * BNB + b * 128 + row_of(h);
+              if (p.bias) add_bias(v, p.bias + (int64_t)t.e * p.N, n0, p.N);
+              uint16_t* out = p.y + orow * p.N + n0;
 #pragma unroll
-              for (int c = 0; c < 8; c++) b[c] = bias ? bf16_to_f32(__ldg(bias + n0 + 8 * i + c)) : 0.f;
-              uint32_t o[4];
-#pragma unroll
-              for (int c = 0; c < 4; c++)
-                o[c] = pack_bf16x2((lo_of(acc[j][4 * i + c]) + b[2 * c]) * w, (hi_of(acc[j][4 * i + c]) + b[2 * c + 1]) * w);
-              *reinterpret_cast<uint4*>(out + n0 + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int i = 0; i < 32; i += 8) {
+                if (n0 + i < p.N)  // N is a multiple of 8
+                  *reinterpret_cast<uint4*>(out + i) =
+                      make_uint4(pack_bf16x2(v[i] * w, v[i + 1] * w), pack_bf16x2(v[i + 2] * w, v[i + 3] * w),
+                                 pack_bf16x2(v[i + 4] * w, v[i + 5] * w), pack_bf16x2(v[i + 6] * w, v[i + 7] * w));
+              }
             }
           }
         }
         continue;
       }
       // gated / plain: activate, agree on each row's largest magnitude per 128 features,
-      // round.  Gated: one group per tile (set 0 gate, set 1 up); plain: two.
+      // round.  Gated: one group per tile (block 0 gate, block 1 up); plain: two.
       constexpr int kGroups = MODE == FP8_GATED ? 1 : 2;
-      float h[kGroups][64];
+      if (live) {
+        const Fp8Bias bias = fp8_bias(MODE, p.layout, t.e, p.N, p.bias, p.gate_bias);
 #pragma unroll
-      for (int j = 0; j < kGroups; j++) {
-        const int f0 = (MODE == FP8_GATED ? t.n_blk * 128 : t.n_blk * BNB + j * 128) + half * 64;
-        float m = 0.f;
-        const Fp8Bias b = fp8_bias(MODE, p.layout, t.e, p.N, p.bias, p.gate_bias);
+        for (int b = 0; b < kGroups; b++) {
+          float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; i++) {
-          const float a0 = i & 1 ? hi_of(acc[j][i / 2]) : lo_of(acc[j][i / 2]);
-          const bool in = f0 + i < p.N;
-          const float g = a0 + (in && b.g ? bf16_to_f32(__ldg(b.g + f0 + i)) : 0.f);
-          if (MODE == FP8_GATED) {
-            const float a1 = i & 1 ? hi_of(acc[1][i / 2]) : lo_of(acc[1][i / 2]);
-            const float up = a1 + (in && b.u ? bf16_to_f32(__ldg(b.u + f0 + i)) : 0.f);
-            h[j][i] = fp8_act(p.act, g, true) * (fp8_up(p.act, up) + p.act.beta);
-          } else {
-            h[j][i] = fp8_act(p.act, g, false);
+          for (int h = 0; h < 2; h++) {
+            float (&g)[32] = *reinterpret_cast<float (*)[32]>(&acc[b][h * 32]);
+            float (&u)[32] = *reinterpret_cast<float (*)[32]>(&acc[1][h * 32]);
+            const int f0 = (MODE == FP8_GATED ? t.n_blk * 128 : t.n_blk * BNB + b * 128) + row_of(h);
+            if (bias.g) add_bias(g, bias.g, f0, p.N);
+            if (bias.u) add_bias(u, bias.u, f0, p.N);
+            m = fmaxf(m, activate<MODE == FP8_GATED>(g, u, p.act, f0, p.N));
           }
-          if (!in) h[j][i] = 0.f;
-          m = fmaxf(m, fabsf(h[j][i]));
+          meta.amax[b][half][r_in_tile] = m;
         }
-        meta.amax[j][half][r_in_tile] = m;
       }
       quadrant_sync(q);
 #pragma unroll
-      for (int j = 0; j < kGroups; j++) {
-        const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + j;
-        const int f0 = grp * 128 + half * 64;
-        const float s = fp8_scale(fmaxf(meta.amax[j][0][r_in_tile], meta.amax[j][1][r_in_tile]));
-        const float inv = __frcp_rn(s);
+      for (int b = 0; b < kGroups; b++) {
+        const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + b;
         if (valid && grp < nbn) {
-          if (half == 0) p.hs[grow * nbn + grp] = s;
-          uint8_t* out = p.hq + grow * p.N + f0;
+          const float s = fp8_scale(fmaxf(meta.amax[b][0][r_in_tile], meta.amax[b][1][r_in_tile]));
+          const float inv = __frcp_rn(s);
+          if (half == 0) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s;
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            if (f0 + 16 * c >= p.N) break;  // N is a multiple of 16
-            uint32_t o[4];
+          for (int h = 0; h < 2; h++) {
+            const int f0 = grp * 128 + row_of(h);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const float* x = &h[j][16 * c + 4 * i];
-              o[i] = fp8_pack4(fp8_quotient(x[0], s, inv), fp8_quotient(x[1], s, inv), fp8_quotient(x[2], s, inv),
-                               fp8_quotient(x[3], s, inv));
+            for (int i = 0; i < 32; i += 16) {
+              if (f0 + i < p.N) {  // N is a multiple of 16
+                const float* x = &acc[b][h * 32 + i];
+                const uint2 lo = fp8_round8(x, s, inv), hi = fp8_round8(x + 8, s, inv);
+                *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0 + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+              }
             }
-            *reinterpret_cast<uint4*>(out + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
       }
@@ -435,10 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();  // both CTAs done: MMAs drained, loads consumed, remote arrivals made
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    if (PAIR) tmem_dealloc_pair(meta.tmem_slot, TMEM_COLS);
+    else tmem_dealloc(meta.tmem_slot, TMEM_COLS);
   }
 }
 
@@ -456,15 +783,54 @@ bool map_stack(CUtensorMap* m, const void* base, uint64_t K, uint64_t N, uint64_
   return map_bytes(m, base, 3, dims, strides, box);
 }
 
-template <int MODE, int ABOX>
+// Pairs of CTAs that can be resident at once on the current device (cached per device).
+template <int MODE>
+int max_pairs(cudaLaunchConfig_t cfg, int num_sms) {
+  static std::atomic<int> cache[64] = {};  // callers may race: each writes the same value
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
+  const int cached = cache[dev].load(std::memory_order_relaxed);
+  if (cached > 0) return cached;
+  int n = 0;
+  cfg.gridDim = dim3(2 * (unsigned)(num_sms / 2), 1, 1);
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<MODE, 128, true>, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    n = num_sms / 2;
+  }
+  cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int MODE, int ABOX, bool PAIR>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& g, const Fp8GemmArgs& p, cudaStream_t st) {
-  const int stages = stages_for(ABOX, p.E);
-  const int smem = 1024 + stages * stage_bytes(ABOX) + meta_bytes(p.E);
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int stages = stages_for(ABOX, PAIR, p.E);
+  const int smem = 1024 + stages * stage_bytes(ABOX, PAIR) + meta_bytes(p.E);
+  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    n++;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   const int64_t units = (int64_t)p.max_tiles * p.splits;
-  const unsigned grid = (unsigned)(units < p.num_sms ? units : p.num_sms);
-  return launch_pdl(fp8_gemm_kernel<MODE, ABOX>, grid, kThreads, smem, st, a, b, g, p, stages);
+  int64_t most = p.num_sms;
+  if constexpr (PAIR) most = max_pairs<MODE>(cfg, p.num_sms);
+  cfg.gridDim = dim3((PAIR ? 2 : 1) * (unsigned)(units < most ? units : most), 1, 1);
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = n + 1;
+  }
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<MODE, ABOX, PAIR>, a, b, g, p, stages);
 }
 
 template <int MODE>
@@ -472,28 +838,30 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
   // no group has more than R rows: small batches load a shorter row tile and leave room
   // for more weight stages (the accumulator rows past it are never stored)
   const uint32_t abox = p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
+  const uint32_t brows = p.pair ? 128 : 64;  // weight rows per box
   CUtensorMap a, b, g;
   const uint64_t dims[2] = {(uint64_t)p.K, (uint64_t)p.R};
   const uint64_t strides[1] = {(uint64_t)p.K};
   const uint32_t box[2] = {BK, abox};
   bool ok = map_bytes(&a, p.a, 2, dims, strides, box);
   if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED) {
-    ok = ok && map_stack(&b, p.w, p.K, p.N, p.E, 128) && map_stack(&g, p.wg, p.K, p.N, p.E, 128);
+    ok = ok && map_stack(&b, p.w, p.K, p.N, p.E, brows) && map_stack(&g, p.wg, p.K, p.N, p.E, brows);
   } else if (MODE == FP8_GATED) {
     const uint64_t K = p.K, N = p.N;
     const uint64_t d4[4] = {K, N, 2, (uint64_t)p.E};
     const uint64_t s4[3] = {K, N * K, 2 * N * K};
-    const uint32_t b4[4] = {BK, 128, 1, 1};
+    const uint32_t b4[4] = {BK, brows, 1, 1};
     ok = ok && map_bytes(&b, p.w, 4, d4, s4, b4);
     g = b;
   } else {
-    ok = ok && map_stack(&b, p.w, p.K, p.N, p.E, BNB);
+    ok = ok && map_stack(&b, p.w, p.K, p.N, p.E, brows);
     g = b;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (abox == 32) return launch<MODE, 32>(a, b, g, p, st);
-  if (abox == 64) return launch<MODE, 64>(a, b, g, p, st);
-  return launch<MODE, 128>(a, b, g, p, st);
+  if (p.pair) return launch<MODE, 128, true>(a, b, g, p, st);
+  if (abox == 32) return launch<MODE, 32, false>(a, b, g, p, st);
+  if (abox == 64) return launch<MODE, 64, false>(a, b, g, p, st);
+  return launch<MODE, 128, false>(a, b, g, p, st);
 }
 
 }  // namespace
@@ -501,6 +869,13 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms) {
   if (R > kSplitMaxRows) return 1;
   return choose_splits(fp8_m_tiles(R, E) * fp8_n_tiles(mode, N), (int)((K + BK - 1) / BK), sms);
+}
+
+bool fp8_pair(int64_t R, int64_t E) {
+  const char* env = std::getenv("MOE_B200_PAIR_FP8");
+  if (env && env[0] == '0') return false;
+  if (env && env[0] == '1') return R > 64;
+  return R > kSplitMaxRows && R >= 512 * E;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, cudaStream_t st) {

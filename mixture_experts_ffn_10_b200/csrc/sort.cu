@@ -43,19 +43,27 @@ __global__ void __launch_bounds__(1024) scan_kernel(SortArgs a) {
   __shared__ int32_t tot;
   pdl_enter();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    // prefixes in place, the loads of kAhead chunks in flight (one after the other they
+    // were most of this kernel: 64 chunks, 21 us)
+    constexpr int kAhead = 16;
     int32_t run = 0;
-    for (int b = 0; b < a.nchunks; b++) {
-      int32_t* p = &a.hist[(int64_t)b * a.E + e];
-      const int32_t h = *p;
-      *p = run;
-      run += h;
+    for (int b0 = 0; b0 < a.nchunks; b0 += kAhead) {
+      int32_t* p = &a.hist[(int64_t)b0 * a.E + e];
+      int32_t h[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) h[i] = b0 + i < a.nchunks ? p[(int64_t)i * a.E] : 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        if (b0 + i < a.nchunks) p[(int64_t)i * a.E] = run;
+        run += h[i];
+      }
     }
     cnt[e] = run;
   }
   segment_scan<2>(a, cnt, tg, td, warp_tot, &tot, ord);
 }
 
-// The whole sort for a single chunk of tokens (T <= kChunkTokens) in one block:
+// The whole sort in one block, for plans with a single chunk (T <= kChunkTokens, or few rows):
 // histogram in shared memory, the segment scan, and the in-order scatter (and the
 // GEMMs' counters cleared).
 __global__ void __launch_bounds__(1024) sort_one_chunk_kernel(SortArgs a) {
