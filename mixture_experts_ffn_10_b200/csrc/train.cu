@@ -23,33 +23,38 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- a token's row
-template <int BF16, int V, int NV>
-struct Row {
-  uint4 v[V > 1 ? NV : 1];
-  float s[V > 1 ? 1 : NV];
+// A token's row in G lanes: lane g holds experts (i G + g) V .. + V - 1, i < NV.
+template <int BF16_, int V_, int NV_, int G_>
+struct Layout {
+  static constexpr int BF16 = BF16_, V = V_, NV = NV_, G = G_, N = V_ * NV_;
+};
 
-  // Experts (i G + lane) V .. + V - 1 for i < NV.
-  __device__ __forceinline__ void load(const void* base, int64_t t, int E, int G, int lane) {
-    if constexpr (V > 1) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + t * E * (16 / V));
+template <class L>
+struct Row {
+  uint4 v[L::V > 1 ? L::NV : 1];
+  float s[L::V > 1 ? 1 : L::NV];
+
+  __device__ __forceinline__ void load(const void* base, int64_t t, int E, int lane) {
+    if constexpr (L::V > 1) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + t * E * (16 / L::V));
 #pragma unroll
-      for (int i = 0; i < NV; i++)
-        if ((i * G + lane) * V < E) v[i] = __ldg(p + i * G + lane);
+      for (int i = 0; i < L::NV; i++)
+        if ((i * L::G + lane) * L::V < E) v[i] = __ldg(p + i * L::G + lane);
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; i++) {
-        const int e = i * G + lane;
+      for (int i = 0; i < L::NV; i++) {
+        const int e = i * L::G + lane;
         if (e < E)
-          s[i] = BF16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(base) + t * E + e))
-                      : __ldg(static_cast<const float*>(base) + t * E + e);
+          s[i] = L::BF16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(base) + t * E + e))
+                         : __ldg(static_cast<const float*>(base) + t * E + e);
       }
     }
   }
   __device__ __forceinline__ float get(int n) const {
-    if constexpr (V == 1) return s[n];
-    const uint4& q = v[n / V];
-    const int c = n % V;
-    if constexpr (BF16) {
+    if constexpr (L::V == 1) return s[n];
+    const uint4& q = v[n / L::V];
+    const int c = n % L::V;
+    if constexpr (L::BF16) {
       const uint32_t u = c < 2 ? q.x : c < 4 ? q.y : c < 6 ? q.z : q.w;
       return __uint_as_float(c & 1 ? u & 0xffff0000u : u << 16);
     } else {
@@ -58,34 +63,47 @@ struct Row {
   }
 };
 
-template <int V>
-__device__ __forceinline__ int expert_of(int n, int G, int lane) {
-  return ((n / V) * G + lane) * V + n % V;
+// Expert of a lane's n-th value; a vector is whole or past E (E is a multiple of V).
+template <class L>
+__device__ __forceinline__ int expert_of(int n, int lane) {
+  return ((n / L::V) * L::G + lane) * L::V + n % L::V;
 }
 
-__device__ __forceinline__ float group_sum(float x, int G) {
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
   for (int o = G >> 1; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-__device__ __forceinline__ float group_max(float x, int G) {
+template <int G>
+__device__ __forceinline__ float group_max(float x) {
+#pragma unroll
   for (int o = G >> 1; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 
-__device__ __forceinline__ float bias_of(const RouterTrainArgs& a, int e) {
-  if (!a.router_bias) return 0.f;
-  return a.bf16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(a.router_bias) + e))
-                : __ldg(static_cast<const float*>(a.router_bias) + e);
+__device__ __forceinline__ float load_one(const void* p, int bf16, int64_t i) {
+  return bf16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(p) + i)) : __ldg(static_cast<const float*>(p) + i);
 }
-__device__ __forceinline__ float logit_of(const RouterTrainArgs& a, int64_t t, int e) {
-  const int64_t i = t * a.E + e;
-  return (a.bf16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(a.logits) + i))
-                 : __ldg(static_cast<const float*>(a.logits) + i)) + bias_of(a, e);
+
+// The router bias of a lane's experts (0 without one, and past E).
+template <class L>
+__device__ __forceinline__ void load_bias(const RouterTrainArgs& a, int lane, float (&b)[L::N]) {
+#pragma unroll
+  for (int n = 0; n < L::N; n++) {
+    const int e = expert_of<L>(n, lane);
+    b[n] = a.router_bias && e < a.E ? load_one(a.router_bias, L::BF16, e) : 0.f;
+  }
 }
+
+// exp and 1 / x by the hardware instructions: 2^-22 relative, exp 2^-24 |x| more (its
+// argument is scaled by log2 e in fp32).
+__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+__device__ __forceinline__ float fast_rcp(float x) { return __fdividef(1.f, x); }
 
 // sigma(l) and 1 - sigma(l), both to full relative precision.
 __device__ __forceinline__ void sigmoid_pair(float l, float* s, float* r) {
-  const float x = expf(-fabsf(l)), d = 1.f / (1.f + x);
+  const float x = fast_exp(-fabsf(l)), d = fast_rcp(1.f + x);
   *s = l >= 0.f ? d : x * d;
   *r = l >= 0.f ? x * d : d;
   if (l != l) *s = *r = l;
@@ -98,41 +116,37 @@ struct Norm {
 };
 
 // l' of the row in l[], scores in s[] (0 past E).  Whole warp.
-template <int BF16, int V, int NV>
-__device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<BF16, V, NV>& row, int G, int lane,
-                                       float (&l)[V * NV], float (&s)[V * NV]) {
-  constexpr int N = V * NV;
+template <class L>
+__device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& row, const float (&bias)[L::N], int lane,
+                                       float (&l)[L::N], float (&s)[L::N]) {
 #pragma unroll
-  for (int n = 0; n < N; n++) {
-    const int e = expert_of<V>(n, G, lane);
-    l[n] = e < a.E ? row.get(n) + bias_of(a, e) : -INFINITY;
-  }
+  for (int n = 0; n < L::N; n++) l[n] = expert_of<L>(n, lane) < a.E ? row.get(n) + bias[n] : -INFINITY;
   Norm z{0.f, 0.f};
   float sum = 0.f;
   if (a.score == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < N; n++) m = fmaxf(m, l[n]);
-    m = group_max(m, G);
+    for (int n = 0; n < L::N; n++) m = fmaxf(m, l[n]);
+    m = group_max<L::G>(m);
     z.m = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int n = 0; n < N; n++) {
-      s[n] = expf(l[n] - z.m);
+    for (int n = 0; n < L::N; n++) {
+      s[n] = fast_exp(l[n] - z.m);
       sum += s[n];
     }
   } else {
 #pragma unroll
-    for (int n = 0; n < N; n++) {
+    for (int n = 0; n < L::N; n++) {
       float r;
       sigmoid_pair(l[n], &s[n], &r);
       sum += s[n];
     }
   }
-  sum = group_sum(sum, G);
+  sum = group_sum<L::G>(sum);
   z.inv_z = sum == 0.f ? 0.f : 1.f / sum;
   if (a.score == MOE_SCORE_SOFTMAX) {
 #pragma unroll
-    for (int n = 0; n < N; n++) s[n] *= z.inv_z;
+    for (int n = 0; n < L::N; n++) s[n] *= z.inv_z;
   }
   return z;
 }
@@ -155,17 +169,19 @@ __device__ __forceinline__ int seq_of(const RouterTrainArgs& a, int t) {
 
 // ---------------------------------------------------------------- balance loss
 constexpr int partial_threads(int n) { return n >= 32 ? 256 : 512; }  // n values of a row per lane
-constexpr int kPartialRows = 16384;  // floats of the block's sums: a row of E per warp
+constexpr int kPartialSums = 8192;  // floats of a block's sums: a row of E per warp
 
-template <int BF16, int V, int NV>
-__global__ void __launch_bounds__(partial_threads(V * NV)) balance_partial_kernel(RouterTrainArgs a, int G) {
-  constexpr int N = V * NV;
+template <class L>
+__global__ void __launch_bounds__(partial_threads(L::N)) balance_partial_kernel(RouterTrainArgs a) {
+  constexpr int G = L::G, N = L::N;
   extern __shared__ float sums[];  // [warps][E], then the histogram [E]
   int32_t* hist = reinterpret_cast<int32_t*>(sums + (blockDim.x >> 5) * a.E);
   pdl_enter();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, groups = blockDim.x / G;
+  const int lane = threadIdx.x % G, group = threadIdx.x / G, groups = blockDim.x / G;
+  float bias[N];
+  load_bias<L>(a, lane, bias);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   for (int b = max(0, seq_of(a, t0)); b < a.B; b++) {
     const int s0 = max(t0, seq_at(a, b)), s1 = min(t1, seq_at(a, b + 1));
@@ -175,15 +191,15 @@ __global__ void __launch_bounds__(partial_threads(V * NV)) balance_partial_kerne
     float acc[N];
 #pragma unroll
     for (int n = 0; n < N; n++) acc[n] = 0.f;
-    Row<BF16, V, NV> next;
+    Row<L> next;
     int t = s0 + group;
-    if (t < s1) next.load(a.logits, t, a.E, G, lane);
+    if (t < s1) next.load(a.logits, t, a.E, lane);
     // the whole warp takes every step (the sums are shuffles)
     for (int base = s0; base < s1; base += groups, t += groups) {
-      const Row<BF16, V, NV> row = next;
-      if (t + groups < s1) next.load(a.logits, t + groups, a.E, G, lane);
+      const Row<L> row = next;
+      if (t + groups < s1) next.load(a.logits, t + groups, a.E, lane);
       float l[N], s[N];
-      const Norm z = scores<BF16, V, NV>(a, row, G, lane, l, s);
+      const Norm z = scores<L>(a, row, bias, lane, l, s);
       const float f = a.score == MOE_SCORE_SOFTMAX ? 1.f : z.inv_z;
       if (t < s1) {
 #pragma unroll
@@ -198,8 +214,9 @@ __global__ void __launch_bounds__(partial_threads(V * NV)) balance_partial_kerne
     // over the groups of the warp, then the warps
 #pragma unroll
     for (int n = 0; n < N; n++) {
+#pragma unroll
       for (int o = G; o < 32; o <<= 1) acc[n] += __shfl_xor_sync(0xffffffffu, acc[n], o);
-      const int e = expert_of<V>(n, G, lane);
+      const int e = expert_of<L>(n, lane);
       if ((threadIdx.x & 31) < G && e < a.E) sums[warp * a.E + e] = acc[n];
     }
     __syncthreads();
@@ -299,14 +316,16 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(RouterTrainArgs a)
 // ---------------------------------------------------------------- backward
 constexpr int kBackThreads = 256;
 
-template <int BF16, int V, int NV>
-__global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTrainArgs a, int G) {
-  constexpr int N = V * NV;
-  extern __shared__ float rows[];  // [groups][G N]
+template <class L>
+__global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTrainArgs a) {
+  constexpr int G = L::G, N = L::N, V = L::V;
+  constexpr int kSlots = N < 32 / G ? N : 32 / G;  // slots per lane: k <= E, k <= 32
+  constexpr int groups = kBackThreads / G;
+  extern __shared__ float4 rows4[];  // [groups][G N] floats
   __shared__ int live_seqs;
   pdl_enter();
-  const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, groups = blockDim.x / G;
-  float* mine = rows + group * G * N;
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  float* mine = reinterpret_cast<float*>(rows4) + group * G * N;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
   float lead = 0.f;  // dloss coef E / k / B'
   if (a.counts) {
@@ -315,64 +334,104 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
     int live = 0;
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) live += seq_at(a, b + 1) > seq_at(a, b);
     live = __reduce_add_sync(0xffffffffu, live);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&live_seqs, live);
+    if ((threadIdx.x & 31) == 0 && live) atomicAdd(&live_seqs, live);
     __syncthreads();
     lead = (a.dloss ? *a.dloss : 1.f) * a.coef * (float)a.E / ((float)a.k * (float)max(live_seqs, 1));
   }
-  const int rounds = (a.k + G - 1) / G;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t t = (int64_t)blockIdx.x * groups + group;
-  Row<BF16, V, NV> next;
-  if (t < a.T) next.load(a.logits, t, a.E, G, lane);
+  float bias[N];
+  load_bias<L>(a, lane, bias);
+  // this block's tokens are neighbours: the sequence and its counts change rarely and stay
+  // in registers
+  const int64_t c0 = (int64_t)blockIdx.x * a.chunk, c1 = min((int64_t)a.T, c0 + a.chunk);
+  int seq_end = -1;    // tokens below it have the amplitude and counts held
+  float amp = 0.f, cnt[N];
+#pragma unroll
+  for (int n = 0; n < N; n++) cnt[n] = 0.f;
+  auto store_row = [&](const float (&x)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; n += V >= 4 ? 4 : 1) {
+      const int e = (n / V) * G * V + lane * V + n % V;
+      if constexpr (V >= 4) *reinterpret_cast<float4*>(mine + e) = make_float4(x[n], x[n + 1], x[n + 2], x[n + 3]);
+      else mine[e] = x[n];
+    }
+  };
+  struct Slots {
+    int e[kSlots];
+    float dw[kSlots];
+  } slots, next_slots;
+  auto load_slots = [&](int64_t t, Slots& s) {
+    if (!a.dw) return;
+#pragma unroll
+    for (int q = 0; q < kSlots; q++) {
+      const int j = q * G + lane;
+      s.e[q] = -1;
+      s.dw[q] = 0.f;
+      if (t < c1 && j < a.k) {
+        const int e = __ldg(a.idx + t * a.k + j);
+        s.e[q] = e >= 0 && e < a.E ? e : -1;
+        s.dw[q] = __ldg(a.dw + t * a.k + j);
+      }
+    }
+  };
+  int64_t t = c0 + group;
+  Row<L> next;
+  if (t < c1) next.load(a.logits, t, a.E, lane);
+  load_slots(t, next_slots);
   // the whole block takes every step (shuffles and warp barriers)
-  for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += step, t += step) {
-    const bool in = t < a.T;
-    const Row<BF16, V, NV> row = next;
-    if (t + step < a.T) next.load(a.logits, t + step, a.E, G, lane);
+  for (int64_t base = c0; base < c1; base += groups, t += groups) {
+    const bool in = t < c1;
+    const Row<L> row = next;
+    slots = next_slots;
+    if (t + groups < c1) next.load(a.logits, t + groups, a.E, lane);
+    load_slots(t + groups, next_slots);
     float l[N], s[N];
-    const Norm z = scores<BF16, V, NV>(a, row, G, lane, l, s);
+    const Norm z = scores<L>(a, row, bias, lane, l, s);
 
     // balance: A (c_e - sum c p), A = 0 for tokens outside every sequence
-    float amp = 0.f, mean = 0.f;
-    const int32_t* c = nullptr;
+    float mean = 0.f;
     if (a.counts) {
-      if (in) {
+      if (in && t >= seq_end) {
         const int b = seq_of(a, (int)t);
-        if (b >= 0 && b < a.B) {
-          const int o0 = seq_at(a, b), o1 = seq_at(a, b + 1);
-          if (t < o1) {
-            const float n = (float)(o1 - o0);
-            amp = lead / (n * n);
-            c = a.counts + (int64_t)b * a.E;
+        amp = 0.f;
+        if (b < 0 || b >= a.B) {
+          seq_end = b < 0 ? seq_at(a, 0) : a.T;
+        } else {
+          const int o0 = seq_at(a, b);
+          seq_end = seq_at(a, b + 1);
+          if (t < seq_end) amp = lead / ((float)(seq_end - o0) * (float)(seq_end - o0));
+          const int32_t* c = a.counts + (int64_t)b * a.E;
+#pragma unroll
+          for (int n = 0; n < N; n++) {
+            const int e = expert_of<L>(n, lane);
+            cnt[n] = e < a.E ? (float)__ldg(c + e) : 0.f;
           }
         }
       }
-      if (c) {
 #pragma unroll
-        for (int n = 0; n < N; n++) {
-          const int e = expert_of<V>(n, G, lane);
-          if (e < a.E) mean += s[n] * (float)__ldg(c + e);
-        }
-      }
-      mean = group_sum(mean, G) * (soft ? 1.f : z.inv_z);
+      for (int n = 0; n < N; n++) mean = fmaf(s[n], cnt[n], mean);
+      mean = group_sum<G>(mean) * (soft ? 1.f : z.inv_z);
     }
 
-    // routing: sums over the slots
-    float kept = 0.f, dot = 0.f;
+    // routing: the slots' scores (softmax) or logits (sigmoid) through the row in shared
+    // memory, and their sums
+    float kept = 0.f, dot = 0.f, ss[kSlots], sr[kSlots];
     if (a.dw) {
-      for (int j = lane; in && j < a.k; j += G) {
-        const int e = __ldg(a.idx + t * a.k + j);
-        if (e >= 0 && e < a.E) {
-          const float le = logit_of(a, t, e);
-          float se, r;
-          if (soft) se = expf(le - z.m) * z.inv_z;
-          else sigmoid_pair(le, &se, &r);
-          kept += se;
-          dot += se * __ldg(a.dw + t * a.k + j);
+      store_row(soft ? s : l);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kSlots; q++) {
+        ss[q] = 0.f;
+        sr[q] = 1.f;
+        if (slots.e[q] >= 0) {
+          ss[q] = mine[slots.e[q]];
+          if (!soft) sigmoid_pair(ss[q], &ss[q], &sr[q]);
         }
+        kept += ss[q];
+        dot = fmaf(ss[q], slots.dw[q], dot);
       }
-      kept = group_sum(kept, G);
-      dot = group_sum(dot, G);
+      kept = group_sum<G>(kept);
+      dot = group_sum<G>(dot);
+      __syncwarp();
     }
     // w_j = S s_j / den: ds_j = S / den (dw_j - [not clamped] dot / den)
     float inv_den = 1.f, shift = 0.f;
@@ -385,40 +444,30 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
     const float drop = soft ? f * (dot - shift * kept) : 0.f;
 
     // the dense part to the row in shared memory, the slots added there
+    float d[N];
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int e = expert_of<V>(n, G, lane);
-      float d = 0.f;
-      if (e < a.E) {
-        const float g = c ? amp * ((float)__ldg(c + e) - mean) : 0.f;
-        if (soft) {
-          d = s[n] * (g - drop);
-        } else if (c) {
-          float se, r;
+      const float g = amp * (cnt[n] - mean);
+      if (soft) {
+        d[n] = s[n] * (g - drop);
+      } else {
+        float r = 0.f;
+        if (a.counts) {
+          float se;
           sigmoid_pair(l[n], &se, &r);
-          d = g * z.inv_z * se * r;
         }
+        d[n] = amp != 0.f ? g * z.inv_z * s[n] * r : 0.f;
       }
-      mine[(n / V) * G * V + lane * V + n % V] = d;
     }
     if (a.dw) {
-      for (int q = 0; q < rounds; q++) {
-        const int j = q * G + lane;
-        int e = -1;
-        float add = 0.f;
-        if (in && j < a.k) {
-          e = __ldg(a.idx + t * a.k + j);
-          if (e < 0 || e >= a.E) e = -1;
-        }
-        if (e >= 0) {
-          const float le = logit_of(a, t, e);
-          float se, r = 1.f;
-          if (soft) se = expf(le - z.m) * z.inv_z;
-          else sigmoid_pair(le, &se, &r);
-          add = f * (__ldg(a.dw + t * a.k + j) - shift) * se * r;
-        }
+      store_row(d);
+#pragma unroll
+      for (int q = 0; q < kSlots; q++) {
+        if (q > 0 && q * G >= a.k) break;
+        const int e = slots.e[q];
+        const float add = f * (slots.dw[q] - shift) * ss[q] * sr[q];
         // slots of one token that name the same expert are added in slot order
-        const unsigned same = __match_any_sync(0xffffffffu, e >= 0 ? (group & 31) * a.E + e : -1 - (int)(threadIdx.x & 31));
+        const unsigned same = __match_any_sync(0xffffffffu, e >= 0 ? (group % 32) * a.E + e : -1 - (int)(threadIdx.x & 31));
         __syncwarp();
         if (__any_sync(0xffffffffu, __popc(same) > 1)) {
           for (int g = 0; g < G; g++) {
@@ -430,99 +479,101 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
         }
         __syncwarp();
       }
-    } else {
-      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < N; n += V >= 4 ? 4 : 1) {
+        const int e = (n / V) * G * V + lane * V + n % V;
+        if constexpr (V >= 4) {
+          const float4 x = *reinterpret_cast<const float4*>(mine + e);
+          d[n] = x.x, d[n + 1] = x.y, d[n + 2] = x.z, d[n + 3] = x.w;
+        } else {
+          d[n] = mine[e];
+        }
+      }
+      __syncwarp();  // the row is read before the next token's is written
     }
     if (in) {
       if constexpr (V > 1) {
         uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dlogits) + t * a.E * (16 / V));
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
+        for (int i = 0; i < L::NV; i++) {
           if ((i * G + lane) * V >= a.E) continue;
-          const float4* m = reinterpret_cast<const float4*>(mine + (i * G + lane) * V);
-          if constexpr (BF16) {
-            const float4 x = m[0], y = m[1];
-            out[i * G + lane] = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
-                                           pack_bf16x2(y.z, y.w));
-          } else {
-            out[i * G + lane] = *reinterpret_cast<const uint4*>(m);
-          }
+          const float* x = &d[i * V];
+          if constexpr (L::BF16)
+            out[i * G + lane] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                           pack_bf16x2(x[6], x[7]));
+          else
+            out[i * G + lane] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                           __float_as_uint(x[3]));
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
+        for (int i = 0; i < L::NV; i++) {
           const int e = i * G + lane;
           if (e >= a.E) continue;
-          if constexpr (BF16) static_cast<uint16_t*>(a.dlogits)[t * a.E + e] = f32_to_bf16_rn(mine[e]);
-          else static_cast<float*>(a.dlogits)[t * a.E + e] = mine[e];
+          if constexpr (L::BF16) static_cast<uint16_t*>(a.dlogits)[t * a.E + e] = f32_to_bf16_rn(d[i]);
+          else static_cast<float*>(a.dlogits)[t * a.E + e] = d[i];
         }
       }
     }
-    __syncwarp();  // the row is read before the next token's is written
   }
 }
 
 // ---------------------------------------------------------------- dispatch
-// Lanes per token: the fewest (a power of two) that hold the row in one vector each.
-int lanes_for(int E, int V) {
-  int G = 1;
-  while (G < 32 && G * V < E) G *= 2;
-  return G;
-}
-
-template <int BF16, int V, int NV>
-cudaError_t run_partial(const RouterTrainArgs& a, int G, cudaStream_t st) {
-  int threads = partial_threads(V * NV);
-  while (threads > 32 && threads / 32 * a.E > kPartialRows / 2) threads /= 2;  // at most 32 KiB of sums
-  // no more groups of lanes than the chunk has tokens
-  while (threads > 128 && threads / 2 / G >= a.chunk) threads /= 2;
-  const size_t smem = (size_t)(threads / 32 + 1) * a.E * 4;
-  return launch_pdl(balance_partial_kernel<BF16, V, NV>, (unsigned)a.nchunks, threads, smem, st, a, G);
-}
-
-template <int BF16, int V, int NV>
-cudaError_t run_backward(const RouterTrainArgs& a, int G, int num_sms, cudaStream_t st) {
-  const int groups = kBackThreads / G;
-  const int64_t blocks = ((int64_t)a.T + groups - 1) / groups, most = (int64_t)num_sms * 8;
-  return launch_pdl(router_backward_kernel<BF16, V, NV>, (unsigned)(blocks < most ? blocks : most), kBackThreads,
-                    (size_t)kBackThreads * V * NV * 4, st, a, G);
-}
-
-template <template <int, int, int> class Run, typename... Args>
-cudaError_t by_row(const RouterTrainArgs& a, Args... rest) {
-  const int V = a.vec ? (a.bf16 ? 8 : 4) : 1;
-  const int G = lanes_for(a.E, V), nv = (a.E + G * V - 1) / (G * V);
-  if (a.vec && a.bf16) {
-    if (nv <= 1) return Run<1, 8, 1>::go(a, G, rest...);
-    if (nv <= 2) return Run<1, 8, 2>::go(a, G, rest...);
-    return Run<1, 8, 4>::go(a, G, rest...);
-  }
-  if (a.vec) {
-    if (nv <= 1) return Run<0, 4, 1>::go(a, G, rest...);
-    if (nv <= 2) return Run<0, 4, 2>::go(a, G, rest...);
-    if (nv <= 4) return Run<0, 4, 4>::go(a, G, rest...);
-    return Run<0, 4, 8>::go(a, G, rest...);
-  }
-  if (a.bf16) {
-    if (nv <= 2) return Run<1, 1, 2>::go(a, G, rest...);
-    if (nv <= 8) return Run<1, 1, 8>::go(a, G, rest...);
-    return Run<1, 1, 32>::go(a, G, rest...);
-  }
-  if (nv <= 2) return Run<0, 1, 2>::go(a, G, rest...);
-  if (nv <= 8) return Run<0, 1, 8>::go(a, G, rest...);
-  return Run<0, 1, 32>::go(a, G, rest...);
-}
-
-template <int BF16, int V, int NV>
+template <class L>
 struct Partial {
-  static cudaError_t go(const RouterTrainArgs& a, int G, cudaStream_t st) { return run_partial<BF16, V, NV>(a, G, st); }
-};
-template <int BF16, int V, int NV>
-struct Backward {
-  static cudaError_t go(const RouterTrainArgs& a, int G, int sms, cudaStream_t st) {
-    return run_backward<BF16, V, NV>(a, G, sms, st);
+  static cudaError_t go(const RouterTrainArgs& a, cudaStream_t st) {
+    int threads = partial_threads(L::N);
+    while (threads > 32 && threads / 32 * a.E > kPartialSums) threads /= 2;
+    // no more groups of lanes than the chunk has tokens
+    while (threads > 128 && threads / 2 / L::G >= a.chunk) threads /= 2;
+    const size_t smem = (size_t)(threads / 32 + 1) * a.E * 4;
+    return launch_pdl(balance_partial_kernel<L>, (unsigned)a.nchunks, threads, smem, st, a);
   }
 };
+template <class L>
+struct Backward {
+  static cudaError_t go(const RouterTrainArgs& a, int sms, cudaStream_t st) {
+    // neighbouring tokens to a block, whole steps of its groups, eight blocks per SM at most
+    constexpr int groups = kBackThreads / L::G;
+    RouterTrainArgs b = a;
+    const int64_t per = ((int64_t)a.T + (int64_t)sms * 8 - 1) / ((int64_t)sms * 8);
+    b.chunk = (int)((per + groups - 1) / groups * groups);
+    return launch_pdl(router_backward_kernel<L>, (unsigned)((a.T + b.chunk - 1) / b.chunk), kBackThreads,
+                      (size_t)kBackThreads * L::N * 4, st, b);
+  }
+};
+
+// One vector per lane on the fewest lanes (a power of two) that hold the row, several on 32.
+template <template <class> class Run, int BF16, typename... Args>
+cudaError_t by_vectors(const RouterTrainArgs& a, Args... rest) {
+  constexpr int V = BF16 ? 8 : 4;
+  const int vectors = a.E / V;
+  if (vectors <= 1) return Run<Layout<BF16, V, 1, 1>>::go(a, rest...);
+  if (vectors <= 2) return Run<Layout<BF16, V, 1, 2>>::go(a, rest...);
+  if (vectors <= 4) return Run<Layout<BF16, V, 1, 4>>::go(a, rest...);
+  if (vectors <= 8) return Run<Layout<BF16, V, 1, 8>>::go(a, rest...);
+  if (vectors <= 16) return Run<Layout<BF16, V, 1, 16>>::go(a, rest...);
+  if (vectors <= 32) return Run<Layout<BF16, V, 1, 32>>::go(a, rest...);
+  if (vectors <= 64) return Run<Layout<BF16, V, 2, 32>>::go(a, rest...);
+  if constexpr (BF16) {
+    return Run<Layout<BF16, V, 4, 32>>::go(a, rest...);
+  } else {
+    if (vectors <= 128) return Run<Layout<BF16, V, 4, 32>>::go(a, rest...);
+    return Run<Layout<BF16, V, 8, 32>>::go(a, rest...);
+  }
+}
+template <template <class> class Run, int BF16, typename... Args>
+cudaError_t by_values(const RouterTrainArgs& a, Args... rest) {
+  if (a.E <= 32) return Run<Layout<BF16, 1, 1, 32>>::go(a, rest...);
+  if (a.E <= 64) return Run<Layout<BF16, 1, 2, 32>>::go(a, rest...);
+  if (a.E <= 256) return Run<Layout<BF16, 1, 8, 32>>::go(a, rest...);
+  return Run<Layout<BF16, 1, 32, 32>>::go(a, rest...);
+}
+template <template <class> class Run, typename... Args>
+cudaError_t by_row(const RouterTrainArgs& a, Args... rest) {
+  if (a.vec) return a.bf16 ? by_vectors<Run, 1>(a, rest...) : by_vectors<Run, 0>(a, rest...);
+  return a.bf16 ? by_values<Run, 1>(a, rest...) : by_values<Run, 0>(a, rest...);
+}
 
 }  // namespace
 

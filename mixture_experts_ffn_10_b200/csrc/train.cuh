@@ -14,8 +14,9 @@ struct RouterTrainArgs {
   const int32_t* seq;        // [B + 1] or null: {0, T}
   int T, E, k, B, bf16, score;
   float coef;
+  int chunk;                 // tokens per block
   // balance loss
-  int chunk, nchunks;        // tokens per block, blocks
+  int nchunks;               // blocks
   float* psum;               // [nchunks + B, E] shares summed per (block, sequence)
   int32_t* pcnt;             // [nchunks + B, E] slots likewise
   double* part;              // [B * E / 32] parts of the loss
