@@ -429,8 +429,7 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
     fa.splits = p.splits_gu;
     fa.partial = gc.partial;
     fa.pitch = gc.partial_pitch;
-    fa.pair = fa.splits == 1 && fp8_pair(p.R, p.E);
-    fa.max_tiles = (int)(fp8_m_tiles(p.R, p.E, fa.pair) * fp8_n_tiles(fa.mode, p.F));
+    fa.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fa.mode, p.F));
     fa.num_sms = num_sms_of_current_device();
     fa.status = status;
     // the bf16 shared expert: the CTA-pair bf16 kernel over the shared segment alone
@@ -478,8 +477,7 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
       fd.y_row = sa.perm;
     }
     fd.splits = p.splits_dn;
-    fd.pair = fd.splits == 1 && fp8_pair(p.R, p.E);
-    fd.max_tiles = (int)(fp8_m_tiles(p.R, p.E, fd.pair) * fp8_n_tiles(fd.mode, p.d));
+    fd.max_tiles = (int)(fp8_m_tiles(p.R, p.E) * fp8_n_tiles(fd.mode, p.d));
     if ((e = launch_fp8_gemm(fd, st)) != cudaSuccess) return cuda_fail(e, "FP8 down GEMM");
     if (p.Fs > 0) {
       sh.c = shared_gemm(p.nt_dn_shared);
@@ -983,7 +981,8 @@ int moe_forward_kernel_count(const moe_shape* s, const moe_options* o) {
   if (moe::gemv_plan(s, p).on) return 1;  // (plus the router GEMM when the layer computes the logits)
   return (p.nchunks == 1 ? 4 : 6) + (p.direct_x ? 0 : 1) + 1 - (p.fused_ffn ? 1 : 0) +
          (s->w_dtype == MOE_MXFP4 && p.Fs > 0 ? 2 : 0) +  // the shared expert beside MXFP4 experts
-         (s->w_dtype == MOE_FP8 ? (p.splits_gu > 1) + (p.Fs > 0 ? 4 : 0) : 0);  // the h reduction; tile lists and GEMMs
+         // FP8: the h reduction, the shared expert's tile lists and GEMMs; no combine of one row
+         (s->w_dtype == MOE_FP8 ? (p.splits_gu > 1) + (p.Fs > 0 ? 4 : 0) - (p.k == 1 && p.Fs == 0 && p.splits_dn == 1) : 0);
 }
 
 int moe_forward_split_k(const moe_shape* s, const moe_options* o, int* splits_gate_up, int* splits_down) {

@@ -36,19 +36,45 @@ inline Fp8Regions fp8_regions(int64_t R, int64_t d, int64_t F, int64_t E) {
 cudaError_t launch_shared_tiles(int32_t* tiles, int E, int n, cudaStream_t st);
 
 // ---------------------------------------------------------------- rounding to e4m3
-// The scale of a block of largest magnitude amax.
-__device__ __forceinline__ float fp8_scale(float amax) { return __fdiv_rn(fmaxf(amax, 0x1p-100f), 448.f); }
+// The scale of a block of largest magnitude amax, max(amax, 2^-100) / 448 correctly rounded:
+// a quotient by the rounded reciprocal, corrected once by its exact remainder (Markstein's
+// division; a fifth of the instructions of __fdiv_rn, which the tests find it equal to).
+// An infinite amax gives an infinite scale.
+__device__ __forceinline__ float fp8_scale(float amax) {
+  constexpr float r = 1.f / 448.f;
+  const float a = fmaxf(amax, 0x1p-100f);
+  const float q = a * r;
+  const float rem = fmaf(-448.f, q, a);
+  return rem == rem ? fmaf(rem, r, q) : q;
+}
+
+// What rounding a block needs: its scale and the scale's reciprocal, a little too small and
+// a little too large (2^-21 relative; the instruction's own error is 2^-23).
+struct Fp8Scale {
+  float s, lo, hi;
+};
+__device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
+  const float s = fp8_scale(amax);
+  const uint32_t u = __float_as_uint(s);
+  if ((u & 0x7fffffu) == 0 && u < 0x7f800000u) {
+    // 2^k: the quotients by it are exact as they are (and ties are frequent)
+    const float inv = __uint_as_float(0x7f000000u - u);
+    return Fp8Scale{s, inv, inv};
+  }
+  const float inv = __fdividef(1.f, s);
+  return Fp8Scale{s, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
+}
 
 // A float that the hardware conversion (nearest even, saturating) takes to the e4m3 value
-// nearest to the real quotient x / s; inv = 1 / s rounded.  t = x inv is within two units
-// in the last place of x / s, so the two round alike unless t lies within a few units of
-// a point halfway between e4m3 values.  Such points (and the e4m3 values) have at most
-// four fraction bits: their low 19 bits are zero.  Next to one, m, the residual x - m s
-// (exact in sign in one fma: m s has 29 bits) tells on which side of m the quotient is.
-__device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
-  float t = x * inv;
-  const uint32_t u = __float_as_uint(t) + 8u;
-  if ((u & 0x7ffffu) < 16u) {
+// nearest to the real quotient x / s.  t = x hi is within eight units in the last place of
+// x / s, so the two round alike unless a point halfway between e4m3 values is that near.
+// Such points (and the e4m3 values) have at most four fraction bits: their low 19 bits are
+// zero.  Next to one, m, the residual x - m s (exact in sign in one fma: m s has 29 bits)
+// tells on which side of m the quotient is.
+static __device__ __noinline__ float fp8_quotient(float x, float s, float hi) {
+  float t = x * hi;
+  const uint32_t u = __float_as_uint(t) + 16u;
+  if ((u & 0x7ffffu) < 32u) {
     const uint32_t m = u & ~0x7ffffu;
     const float r = fmaf(-__uint_as_float(m), s, x);  // NaN (t stays) for NaN x and for infinite s
     const bool neg = (m >> 31) != 0;
@@ -59,33 +85,22 @@ __device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
   return t;
 }
 
-// The same for eight values at once, as e4m3 (the first in the low byte).  The quotients
-// x inv round as they are unless one is next to a halfway point: 2^-6 and above those have
-// the low 20 bits 0x80000, below it (steps of 2^-9) they are left to fp8_quotient.
-__device__ __forceinline__ uint2 fp8_round8(const float* x, float s, float inv);
-
-// Four quotients as e4m3, the first in the low byte.
+// Four floats as e4m3, the first in the low byte.
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 
-__device__ __forceinline__ uint2 fp8_round8(const float* x, float s, float inv) {
-  float t[8];
-  bool near = false;
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    t[i] = x[i] * inv;
-    const uint32_t u = __float_as_uint(t[i]);
-    near |= ((u - 0x7fff8u) & 0xfffffu) < 16u;               // within 8 units of a halfway point
-    near |= 2u * u - 1u < 2u * __float_as_uint(0x1p-6f) - 1u;  // small, and not zero
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) t[i] = fp8_quotient(x[i], s, inv);
-  }
-  return make_uint2(fp8_pack4(t[0], t[1], t[2], t[3]), fp8_pack4(t[4], t[5], t[6], t[7]));
+// x[0 .. 3] / s as e4m3.  The real quotients lie between x lo and x hi; rounding is
+// monotone, so where both round to the same value, that is the answer (all but a few in ten
+// thousand: no test of each value for the neighbourhood of a halfway point is needed).
+__device__ __forceinline__ uint32_t fp8_round4(const float* x, const Fp8Scale& f) {
+  const uint32_t lo = fp8_pack4(x[0] * f.lo, x[1] * f.lo, x[2] * f.lo, x[3] * f.lo);
+  const uint32_t hi = fp8_pack4(x[0] * f.hi, x[1] * f.hi, x[2] * f.hi, x[3] * f.hi);
+  if (lo == hi) return hi;
+  return fp8_pack4(fp8_quotient(x[0], f.s, f.hi), fp8_quotient(x[1], f.s, f.hi), fp8_quotient(x[2], f.s, f.hi),
+                   fp8_quotient(x[3], f.s, f.hi));
 }
 
 // ---------------------------------------------------------------- activation
@@ -174,7 +189,6 @@ struct Fp8GemmArgs {
   int splits;
   float* partial;
   int pitch;
-  int pair;                   // CTA pairs: tiles of 256 rows (no splits)
   int max_tiles;              // upper bound of the tile count
   int num_sms;
   int* status;
@@ -185,11 +199,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 // N tiles of a GEMM: 256 accumulator columns (128 gated features).
 inline int fp8_n_tiles(int mode, int64_t N) { return (int)((N + (mode == FP8_GATED ? 127 : 255)) / (mode == FP8_GATED ? 128 : 256)); }
 // Upper bound of the row tiles of R rows in E groups: every group adds at most one partial tile.
-inline int64_t fp8_m_tiles(int64_t R, int64_t E, bool pair = false) {
-  return R / (pair ? 2 * kFp8BM : kFp8BM) + (E < R ? E : R);
-}
-// Whether the GEMMs run on CTA pairs.
-bool fp8_pair(int64_t R, int64_t E);
+inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return R / kFp8BM + (E < R ? E : R); }
 // The split factor of a GEMM (1: none).
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms);
 

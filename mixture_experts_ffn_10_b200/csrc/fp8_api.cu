@@ -133,8 +133,7 @@ int moe_fp8_matmul(int64_t rows, int64_t E, int64_t N, int64_t K, const uint8_t*
   a.clear_status = 1;
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
   a.pitch = fp8_n_tiles(FP8_LINEAR, N) * 256;
-  a.pair = splits == 1 && fp8_pair(rows, E);
-  a.max_tiles = (int)(fp8_m_tiles(rows, E, a.pair) * fp8_n_tiles(FP8_LINEAR, N));
+  a.max_tiles = (int)(fp8_m_tiles(rows, E) * fp8_n_tiles(FP8_LINEAR, N));
   a.num_sms = device_sms();
   cudaError_t e = launch_fp8_gemm(a, st);
   if (e != cudaSuccess) return cuda_status(e, "FP8 grouped GEMM");

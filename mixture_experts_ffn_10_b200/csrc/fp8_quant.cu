@@ -2,11 +2,10 @@
 // activations) or per 128 x 128 block (weights), and the gather that quantises the
 // layer's tokens into expert order.
 //
-//   s = max(amax, 2^-100) / 448,  q = e4m3(x / s)   (fp8_scale, fp8_quotient)
+//   s = max(amax, 2^-100) / 448,  q = e4m3(x / s)   (fp8_scale, fp8_round4)
 //
-// One pass: the 128 columns of a block stay in the registers of 16 lanes (bf16, eight
-// values each) or 32 lanes (fp32, four each) between the maximum and the rounding, so
-// each value is read once and its byte written once.  Bound by memory.
+// One pass: the 128 columns of a block stay in the registers of eight lanes between the
+// maximum and the rounding, so each value is read once and its byte written once.
 #include "fp8.cuh"
 
 namespace moe {
@@ -14,26 +13,43 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A lane's 16 bytes as floats: V = 8 bf16 or 4 fp32.
-template <int V>
-__device__ __forceinline__ void unpack16(const uint4& q, float (&f)[V]) {
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+// 16 neighbouring values of a row in one lane, as loaded: two (bf16) or four (fp32)
+// vectors of 16 bytes, zeros past K.
+template <bool BF16>
+struct Sixteen {
+  static constexpr int kVecs = BF16 ? 2 : 4, kPer = 16 / kVecs;  // vectors, values in each
+  uint4 v[kVecs];
+
+  __device__ __forceinline__ void load(const void* row, int col, int K) {  // col: the lane's first column
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (int64_t)col * (BF16 ? 2 : 4));
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if constexpr (V == 8) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    } else {
-      f[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < kVecs; i++) v[i] = col + i * kPer < K ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kVecs; i++) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void unpack(float (&f)[16]) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; i++) {
+      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        if constexpr (BF16) {
+          f[8 * i + 2 * c] = __uint_as_float(u[c] << 16);
+          f[8 * i + 2 * c + 1] = __uint_as_float(u[c] & 0xffff0000u);
+        } else {
+          f[4 * i + c] = __uint_as_float(u[c]);
+        }
+      }
     }
   }
-}
+};
 
-template <int V>
-__device__ __forceinline__ float amax_of(const float (&f)[V]) {
+__device__ __forceinline__ float amax16(const float (&f)[16]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; i++) m = fmaxf(m, fabsf(f[i]));
+  for (int i = 0; i < 16; i++) m = fmaxf(m, fabsf(f[i]));  // (a NaN is left out)
   return m;
 }
 
@@ -45,54 +61,66 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
-template <int V>
-__device__ __forceinline__ void store_q(uint8_t* dst, const float (&f)[V], float s, float inv) {
-  if constexpr (V == 8)
-    *reinterpret_cast<uint2*>(dst) = fp8_round8(f, s, inv);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = fp8_pack4(fp8_quotient(f[0], s, inv), fp8_quotient(f[1], s, inv),
-                                                  fp8_quotient(f[2], s, inv), fp8_quotient(f[3], s, inv));
+// The lane's 16 values rounded, to q (its first column's place): whole, or (rows of a
+// multiple of 8 or 4 values) the vectors below K.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store16(uint8_t* q, int col, int K, const float (&f)[16], const Fp8Scale& s) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] = fp8_round4(f + 4 * i, s);
+  if constexpr (WHOLE) {
+    if (col < K) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if constexpr (BF16) {
+    if (col < K) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    if (col + 8 < K) *reinterpret_cast<uint2*>(q + 8) = make_uint2(w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (col + 4 * i < K) *reinterpret_cast<uint32_t*>(q + 4 * i) = w[i];
+  }
 }
 
-// Vectorised rows: 128 / V lanes per block, kBatch blocks in flight per group of lanes.
-constexpr int kBatch = 4;
-template <int V>
+// Rows in vectors: eight lanes per block of 128 columns, so that a block's maximum and
+// scale are worked out by eight lanes for 16 values each; two blocks in flight.  With eight
+// values per lane the kernel was bound by instructions (183 per eight values, 16384 rows of
+// 7168: 113 us).
+constexpr int kLanes = 8, kGroups = kThreads / kLanes, kBatch = 2;
+template <bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const uint8_t* x, int64_t pitch_bytes, int K, int nb,
-                                                                 int64_t blocks, uint8_t* q, float* scales) {
+                                                                 int step_row, int step_blk, int64_t blocks, uint8_t* q,
+                                                                 float* scales) {
   pdl_enter();
-  constexpr int L = 128 / V;
-  constexpr int kGroups = kThreads / L;
-  const int sub = threadIdx.x / L, lane = threadIdx.x % L;
-  const int64_t b0 = (int64_t)blockIdx.x * (kGroups * kBatch) + sub;
-  uint4 v[kBatch];
+  const int64_t b0 = (int64_t)blockIdx.x * (kGroups * kBatch) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  // one division, then steps of kGroups blocks
   int64_t row[kBatch];
   int col[kBatch];
-  const int64_t first = b0 / nb;  // one division, then steps of kGroups blocks
-  int down = 0, blk = (int)(b0 - first * nb);
+  row[0] = b0 / nb;
+  int blk = (int)(b0 - row[0] * nb);
+  Sixteen<BF16> v[kBatch];
 #pragma unroll
   for (int i = 0; i < kBatch; i++) {
-    const int64_t b = b0 + i * kGroups;
-    row[i] = first + down;
-    col[i] = blk * 128 + lane * V;
-    blk += kGroups;
-    while (blk >= nb) {
-      blk -= nb;
-      down++;
+    col[i] = blk * 128 + lane * 16;
+    if (b0 + i * kGroups < blocks) v[i].load(x + row[i] * pitch_bytes, col[i], K);
+    else v[i].clear();
+    if (i + 1 < kBatch) {
+      blk += step_blk;
+      row[i + 1] = row[i] + step_row;
+      if (blk >= nb) {
+        blk -= nb;
+        row[i + 1]++;
+      }
     }
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (b < blocks && col[i] < K)
-      v[i] = __ldg(reinterpret_cast<const uint4*>(x + row[i] * pitch_bytes + (int64_t)col[i] * (16 / V)));
   }
 #pragma unroll
   for (int i = 0; i < kBatch; i++) {
     const int64_t b = b0 + i * kGroups;
-    float f[V];
-    unpack16<V>(v[i], f);
-    const float s = fp8_scale(lanes_max<L>(amax_of<V>(f)));
-    const float inv = __frcp_rn(s);
+    float f[16];
+    v[i].unpack(f);
+    const Fp8Scale s = fp8_scale_of(lanes_max<kLanes>(amax16(f)));
     if (b < blocks) {
-      if (col[i] < K) store_q<V>(q + row[i] * K + col[i], f, s, inv);
-      if (lane == 0) scales[b] = s;
+      store16<BF16, WHOLE>(q + row[i] * K + col[i], col[i], K, f, s);
+      if (lane == 0) scales[b] = s.s;
     }
   }
 }
@@ -113,41 +141,40 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_any_kernel(const void*
   float f[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) f[i] = c0 + 32 * i < K ? load_any(x, bf16, row * pitch + c0 + 32 * i) : 0.f;
-  const float s = fp8_scale(lanes_max<32>(amax_of<4>(f)));
-  const float inv = __frcp_rn(s);
+  const Fp8Scale s = fp8_scale_of(lanes_max<32>(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])))));
+  const uint32_t w = fp8_round4(f, s);
 #pragma unroll
   for (int i = 0; i < 4; i++)
-    if (c0 + 32 * i < K)
-      q[row * K + c0 + 32 * i] = (uint8_t)fp8_pack4(fp8_quotient(f[i], s, inv), 0.f, 0.f, 0.f);
-  if (lane == 0) scales[b] = s;
+    if (c0 + 32 * i < K) q[row * K + c0 + 32 * i] = (uint8_t)(w >> (8 * i));
+  if (lane == 0) scales[b] = s.s;
 }
 
-// One 128 x 128 weight block per thread block.  Vectorised rows are held in registers
-// between the maximum and the rounding (64 values per thread).
-template <int V>
+// One 128 x 128 weight block per thread block, held in registers between the maximum and
+// the rounding (64 values per thread).
+template <bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) quantize_weights_kernel(const uint8_t* w, int64_t N, int64_t K, int nbn, int nbk,
                                                                     uint8_t* q, float* scales) {
   pdl_enter();
   __shared__ float warp_max[kThreads / 32];
-  constexpr int L = 128 / V, kRows = kThreads / L, kIter = 128 / kRows;  // rows per step, steps
+  constexpr int kIter = 128 / kGroups;  // steps of kGroups rows
   const int64_t blk = blockIdx.x;
   const int kb = (int)(blk % nbk);
   const int64_t en = blk / nbk, e = en / nbn;
   const int64_t n0 = (en - e * nbn) * 128;
-  const int col = kb * 128 + (threadIdx.x % L) * V, r0 = threadIdx.x / L;
-  uint4 v[kIter];
+  const int col = kb * 128 + (threadIdx.x % kLanes) * 16, r0 = threadIdx.x / kLanes;
+  Sixteen<BF16> v[kIter];
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < kIter; i++) {
-    const int64_t n = n0 + r0 + i * kRows;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (n < N && col < K) v[i] = __ldg(reinterpret_cast<const uint4*>(w + ((e * N + n) * K + col) * (16 / V)));
+    const int64_t n = n0 + r0 + i * kGroups;
+    if (n < N) v[i].load(w + (e * N + n) * K * (BF16 ? 2 : 4), col, (int)K);
+    else v[i].clear();
   }
 #pragma unroll
   for (int i = 0; i < kIter; i++) {
-    float f[V];
-    unpack16<V>(v[i], f);
-    m = fmaxf(m, amax_of<V>(f));
+    float f[16];
+    v[i].unpack(f);
+    m = fmaxf(m, amax16(f));
   }
   m = lanes_max<32>(m);
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
@@ -155,15 +182,15 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_kernel(const uint8_
   m = warp_max[0];
 #pragma unroll
   for (int i = 1; i < kThreads / 32; i++) m = fmaxf(m, warp_max[i]);
-  const float s = fp8_scale(m), inv = __frcp_rn(s);
+  const Fp8Scale s = fp8_scale_of(m);
 #pragma unroll
   for (int i = 0; i < kIter; i++) {
-    const int64_t n = n0 + r0 + i * kRows;
-    float f[V];
-    unpack16<V>(v[i], f);
-    if (n < N && col < K) store_q<V>(q + (e * N + n) * K + col, f, s, inv);
+    const int64_t n = n0 + r0 + i * kGroups;
+    float f[16];
+    v[i].unpack(f);
+    if (n < N) store16<BF16, WHOLE>(q + (e * N + n) * K + col, col, (int)K, f, s);
   }
-  if (threadIdx.x == 0) scales[blk] = s;
+  if (threadIdx.x == 0) scales[blk] = s.s;
 }
 
 // The same for rows of any size and alignment, reading the block twice.
@@ -185,50 +212,52 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_any_kernel(const vo
   __syncthreads();
   m = warp_max[0];
   for (int i = 1; i < kThreads / 32; i++) m = fmaxf(m, warp_max[i]);
-  const float s = fp8_scale(m), inv = __frcp_rn(s);
+  const Fp8Scale s = fp8_scale_of(m);
   for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
     const int64_t at = base + (int64_t)(i / cols) * K + i % cols;
-    q[at] = (uint8_t)fp8_pack4(fp8_quotient(load_any(w, bf16, at), s, inv), 0.f, 0.f, 0.f);
+    q[at] = (uint8_t)fp8_pack4(fp8_quotient(load_any(w, bf16, at), s.s, s.hi), 0.f, 0.f, 0.f);
   }
-  if (threadIdx.x == 0) scales[blk] = s;
+  if (threadIdx.x == 0) scales[blk] = s.s;
 }
 
-// Tokens into expert order: 16 lanes per (token, block of 128 columns), which is read
+// Tokens into expert order: eight lanes per (token, block of 128 columns), which is read
 // and rounded once and written to the token's k rows (rounded per row for weigh-inputs,
 // whose rows differ by their weight); B blocks in flight per group of lanes.
 template <int B>
-__global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs a, int nb) {
+__global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs a, int nb, int step_t, int step_blk) {
   pdl_enter();
-  constexpr int kGroups = kThreads / 16;
-  const int64_t b0 = (int64_t)blockIdx.x * (kGroups * B) + threadIdx.x / 16;
-  const int lane = threadIdx.x & 15;
-  const int first = (int)(b0 / nb);  // one division, then steps of kGroups blocks
-  int blk = (int)(b0 - (int64_t)first * nb), t = first;
-  uint4 v[B];
+  const int64_t b0 = (int64_t)blockIdx.x * (kGroups * B) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
   int tok[B], at[B];
+  tok[0] = (int)(b0 / nb);
+  at[0] = (int)(b0 - (int64_t)tok[0] * nb);
+  Sixteen<true> v[B];
 #pragma unroll
   for (int i = 0; i < B; i++) {
-    tok[i] = t;
-    at[i] = blk;
-    const int col = blk * 128 + lane * 8;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (t < a.T && col < a.d) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d + col));
-    blk += kGroups;
-    while (blk >= nb) {
-      blk -= nb;
-      t++;
+    if (tok[i] < a.T) v[i].load(a.x + (int64_t)tok[i] * a.d, at[i] * 128 + lane * 16, a.d);
+    else v[i].clear();
+    if (i + 1 < B) {
+      at[i + 1] = at[i] + step_blk;
+      tok[i + 1] = tok[i] + step_t;
+      if (at[i + 1] >= nb) {
+        at[i + 1] -= nb;
+        tok[i + 1]++;
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < B; i++) {
-    const int col = at[i] * 128 + lane * 8;
-    float f[8];
-    unpack16<8>(v[i], f);
-    const float m = lanes_max<16>(amax_of<8>(f));
-    if (tok[i] >= a.T) continue;  // (the shuffles are behind: lanes of a group agree, groups need not)
-    float s = fp8_scale(m), inv = __frcp_rn(s);
-    uint2 w = make_uint2(0, 0);
-    if (!a.weigh_inputs) w = fp8_round8(f, s, inv);
+    const int col = at[i] * 128 + lane * 16;
+    float f[16];
+    v[i].unpack(f);
+    const float m = lanes_max<kLanes>(amax16(f));
+    if (tok[i] >= a.T) continue;
+    Fp8Scale s = fp8_scale_of(m);
+    uint32_t w[4] = {};
+    if (!a.weigh_inputs) {
+#pragma unroll
+      for (int c = 0; c < 4; c++) w[c] = fp8_round4(f + 4 * c, s);
+    }
     for (int j = 0; j < a.k; j++) {
       const int row = a.pos[(int64_t)tok[i] * a.k + j];
       if (row < 0 || row >= a.R) {
@@ -238,15 +267,16 @@ __global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs
       if (a.weigh_inputs) {
         // the largest |w x| is |w| times the largest |x| (rounding is monotone)
         const float wt = a.roww[row];
-        float g[8];
+        float g[16];
 #pragma unroll
-        for (int c = 0; c < 8; c++) g[c] = f[c] * wt;
-        s = fp8_scale(fabsf(m * wt));
-        inv = __frcp_rn(s);
-        w = fp8_round8(g, s, inv);
+        for (int c = 0; c < 16; c++) g[c] = f[c] * wt;
+        s = fp8_scale_of(fabsf(m * wt));
+#pragma unroll
+        for (int c = 0; c < 4; c++) w[c] = fp8_round4(g + 4 * c, s);
       }
-      if (col < a.d) *reinterpret_cast<uint2*>(a.xq + (int64_t)row * a.d + col) = w;
-      if (lane == 0) a.xs[(int64_t)at[i] * a.R + row] = s;
+      // d is a multiple of 16
+      if (col < a.d) *reinterpret_cast<uint4*>(a.xq + (int64_t)row * a.d + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (lane == 0) a.xs[(int64_t)at[i] * a.R + row] = s.s;
     }
   }
 }
@@ -265,12 +295,14 @@ cudaError_t launch_fp8_quantize(int bf16, int64_t rows, int64_t K, const void* x
   const int nb = (int)((K + 127) / 128);
   const int64_t blocks = rows * nb;
   const int V = bf16 ? 8 : 4, elt = bf16 ? 2 : 4;
-  // sixteen bytes per lane: whole vectors in every row of x, whole words of q
+  // sixteen bytes per load: whole vectors in every row of x, whole words of q
   if (K % V == 0 && (pitch * elt) % 16 == 0 && aligned(x, 16) && aligned(q, V)) {
-    const int per = kThreads / (128 / V) * kBatch;
-    const unsigned grid = (unsigned)((blocks + per - 1) / per);
-    return launch_pdl(bf16 ? quantize_rows_kernel<8> : quantize_rows_kernel<4>, grid, kThreads, 0, st, (const uint8_t*)x,
-                      pitch * elt, (int)K, nb, blocks, q, scales);
+    const bool whole = K % 16 == 0 && aligned(q, 16);
+    const auto kernel = bf16 ? (whole ? quantize_rows_kernel<true, true> : quantize_rows_kernel<true, false>)
+                             : (whole ? quantize_rows_kernel<false, true> : quantize_rows_kernel<false, false>);
+    const int per = kGroups * kBatch;
+    return launch_pdl(kernel, (unsigned)((blocks + per - 1) / per), kThreads, 0, st, (const uint8_t*)x, pitch * elt, (int)K, nb,
+                      kGroups / nb, kGroups % nb, blocks, q, scales);
   }
   const unsigned grid = (unsigned)((blocks + kThreads / 32 - 1) / (kThreads / 32));
   return launch_pdl(quantize_rows_any_kernel, grid, kThreads, 0, st, x, bf16, pitch, (int)K, nb, blocks, q, scales);
@@ -280,9 +312,12 @@ cudaError_t launch_fp8_quantize_weights(int bf16, int64_t E, int64_t N, int64_t 
                                         cudaStream_t st) {
   const int nbn = (int)((N + 127) / 128), nbk = (int)((K + 127) / 128);
   const unsigned grid = (unsigned)(E * nbn * nbk);
-  if (K % (bf16 ? 8 : 4) == 0 && aligned(w, 16) && aligned(q, bf16 ? 8 : 4))
-    return launch_pdl(bf16 ? quantize_weights_kernel<8> : quantize_weights_kernel<4>, grid, kThreads, 0, st,
-                      (const uint8_t*)w, N, K, nbn, nbk, q, scales);
+  if (K % (bf16 ? 8 : 4) == 0 && aligned(w, 16) && aligned(q, bf16 ? 8 : 4)) {
+    const bool whole = K % 16 == 0 && aligned(q, 16);
+    const auto kernel = bf16 ? (whole ? quantize_weights_kernel<true, true> : quantize_weights_kernel<true, false>)
+                             : (whole ? quantize_weights_kernel<false, true> : quantize_weights_kernel<false, false>);
+    return launch_pdl(kernel, grid, kThreads, 0, st, (const uint8_t*)w, N, K, nbn, nbk, q, scales);
+  }
   return launch_pdl(quantize_weights_any_kernel, grid, kThreads, 0, st, w, bf16, N, K, nbn, nbk, q, scales);
 }
 
@@ -293,11 +328,12 @@ cudaError_t launch_shared_tiles(int32_t* tiles, int E, int n, cudaStream_t st) {
 cudaError_t launch_fp8_gather(const Fp8GatherArgs& a, cudaStream_t st) {
   if (a.R == 0) return cudaSuccess;
   const int nb = (a.d + 127) / 128;
-  // four blocks in flight once that leaves every SM several thread blocks
-  const int64_t work = (int64_t)a.T * nb, per = kThreads / 16;
-  if (work >= per * 4 * 592)
-    return launch_pdl(gather_quantize_kernel<4>, (unsigned)((work + 4 * per - 1) / (4 * per)), kThreads, 0, st, a, nb);
-  return launch_pdl(gather_quantize_kernel<1>, (unsigned)((work + per - 1) / per), kThreads, 0, st, a, nb);
+  // two blocks in flight once that leaves every SM several thread blocks
+  const int64_t work = (int64_t)a.T * nb;
+  const int sr = kGroups / nb, sb = kGroups % nb;
+  if (work >= kGroups * 2 * 592)
+    return launch_pdl(gather_quantize_kernel<2>, (unsigned)((work + 2 * kGroups - 1) / (2 * kGroups)), kThreads, 0, st, a, nb, sr, sb);
+  return launch_pdl(gather_quantize_kernel<1>, (unsigned)((work + kGroups - 1) / kGroups), kThreads, 0, st, a, nb, sr, sb);
 }
 
 }  // namespace moe

@@ -77,12 +77,9 @@ __global__ void __launch_bounds__(kThreads) reduce_h_kernel(Fp8GemmArgs a, const
   float m = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s = fp8_scale(m), inv = __frcp_rn(s);
-  if (in)
-    *reinterpret_cast<uint32_t*>(a.hq + (int64_t)row * a.N + f0) =
-        fp8_pack4(fp8_quotient(h[0], s, inv), fp8_quotient(h[1], s, inv), fp8_quotient(h[2], s, inv),
-                  fp8_quotient(h[3], s, inv));
-  if (lane == 0) a.hs[row * a.hs_row + grp * a.hs_grp] = s;
+  const Fp8Scale s = fp8_scale_of(m);
+  if (in) *reinterpret_cast<uint32_t*>(a.hq + (int64_t)row * a.N + f0) = fp8_round4(h, s);
+  if (lane == 0) a.hs[row * a.hs_row + grp * a.hs_grp] = s.s;
 }
 
 // Four outputs per thread; the rows of the groups only.

@@ -16,21 +16,19 @@
 // with two halves of 256 columns the chain product - hand-over - adds - hand-over of a
 // buffer was longer than two products.
 //
-// Work: tiles of 256 weight rows (128 gate and their 128 up rows, or 256 plain rows) by
-// 128 rows on one CTA, or by 256 rows on a CTA pair (cta_group::2, each CTA staging its
-// 128 rows and half of the weights); persistent CTAs, one per SM; the tile list is made on
-// the device from the groups' row counts.  Warps of a CTA:
+// Work: tiles of 128 rows by 256 weight rows (128 gate and their 128 up rows, or 256 plain
+// rows); persistent CTAs, one per SM; the tile list is made on the device from the groups'
+// row counts.  (On CTA pairs, 256 rows by 256 weight rows, the kernel loaded a third less
+// and was no faster: 8192 rows of 8 experts of 4096 x 14336 took 1.81 ms against 1.71, the
+// adds and the power limit being the bound.)  Warps of a CTA:
 //   0     TMA producer (128-byte swizzle, one block of K per stage);
-//   1, 3  MMA issue (of a pair: in the even CTA), blocks of K in turn; 1: TMEM, too;
+//   1, 3  MMA issue, blocks of K in turn; 1: TMEM, too;
 //   2     the products of row and weight scales, a ring of blocks ahead in shared memory
 //         (read by the epilogue itself they cost it a memory latency per block);
 //   4-11  epilogue: TMEM lane quadrant x column half.  Their accumulators do not fit the
 //         168 registers that twelve warps leave each: the first four warps hand theirs
-//         over (setmaxnreg, 4 x 88 + 8 x 208 = 12 x 168).
+//         over (setmaxnreg, 4 x 104 + 8 x 200 = 12 x 168).
 // Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.
-#include <atomic>
-#include <cstdlib>
-
 #include "fp8.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -49,17 +47,14 @@ constexpr int TMEM_COLS = kQuarters * BNH;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
-constexpr int kControlRegs = 88, kEpiRegs = 208;  // of 168 at launch: 4 x 88 + 8 x 208 = 12 x 168
+constexpr int kControlRegs = 104, kEpiRegs = 200;  // of 168 at launch: 4 x 104 + 8 x 200 = 12 x 168
 constexpr int kMaxStages = 6;
 constexpr int kScaleBatch = 8;    // blocks of K whose scale products are handed over together
 constexpr int kScaleSlots = 2 * kScaleBatch;
 constexpr int kSmemLimit = 232448;
 // kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B e4m3 (format 0), K-major, N >> 3
-// in bits 17-22, M >> 4 in 24-28 (M = 128, or 256 over a pair).
-constexpr uint32_t idesc(bool pair) {
-  return (1u << 4) | ((uint32_t)(BNH >> 3) << 17) | ((uint32_t)((pair ? 2 * BM : BM) >> 4) << 24);
-}
-constexpr uint16_t kBothCtas = 0x3, kEvenCta = 0x1;
+// in bits 17-22, M >> 4 in 24-28.
+constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BNH >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 
 // Shared memory after the stages: scale products, barriers, the row maxima the two column
 // halves of a tile exchange, the groups' first rows and tile prefixes.  The quarters'
@@ -73,35 +68,20 @@ struct alignas(64) Meta {
   int abort_flag;
 };
 
-constexpr int stage_bytes(int abox, bool pair) { return (abox + (pair ? BNB / 2 : BNB)) * BK; }
+constexpr int stage_bytes(int abox) { return (abox + BNB) * BK; }
 constexpr int meta_bytes(int E) { return (int)sizeof(Meta) + 2 * (E + 1) * 4; }
-constexpr int stages_for(int abox, bool pair, int E) {
-  const int n = (kSmemLimit - 1024 - meta_bytes(E)) / stage_bytes(abox, pair);
+constexpr int stages_for(int abox, int E) {
+  const int n = (kSmemLimit - 1024 - meta_bytes(E)) / stage_bytes(abox);
   return n > kMaxStages ? kMaxStages : n;
 }
 
-template <bool PAIR>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc(true)), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc(false)), "r"(accumulate)
-        : "memory");
-}
-// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued before have completed.
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if constexpr (PAIR) mma_commit_pair(bar, kBothCtas);
-  else mma_commit(bar);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
+      : "memory");
 }
 
 // Waits for the thread's TMEM loads; r is in place after it (and not read before).
@@ -183,23 +163,11 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
       "r"(lane)
       : "memory");
 }
-// The same on a barrier of either CTA of a pair, to hand over tensor memory only (read to
-// registers, fenced).  With release semantics it would wait for the thread's other memory
-// operations, and the epilogue makes one per quarter.
-__device__ __forceinline__ void warp_arrive_cluster_relaxed(uint32_t bar_cluster, int lane) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar_cluster),
-      "r"(lane)
-      : "memory");
-}
-
 struct Unit {
   int e, m0, n_blk, rows, row0, sp, kb0, kb1;
 };
 
 // Unit u of the list: split-fastest, then row tile, then N block, then group.
-template <int BMT>  // rows per tile
 __device__ __forceinline__ Unit unit_of(const Fp8GemmArgs& p, const int32_t* row0, const int32_t* tiles, int u, int nkb) {
   Unit r;
   const int tile = u / p.splits;
@@ -213,10 +181,10 @@ __device__ __forceinline__ Unit unit_of(const Fp8GemmArgs& p, const int32_t* row
   r.e = lo;
   r.row0 = row0[lo];
   r.rows = row0[lo + 1] - r.row0;
-  const int mt = (r.rows + BMT - 1) / BMT;
+  const int mt = (r.rows + BM - 1) / BM;
   const int local = tile - tiles[lo];
   r.n_blk = local / mt;
-  r.m0 = (local % mt) * BMT;
+  r.m0 = (local % mt) * BM;
   r.kb0 = r.sp * nkb / p.splits;
   r.kb1 = (r.sp + 1) * nkb / p.splits;
   return r;
@@ -247,14 +215,24 @@ template <bool GATED, int ACT>
 __device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], const ActParams& act, int f0, int N) {
   ActParams a = act;
   a.act = ACT;
+  if (ACT == MOE_ACT_SILU && GATED && a.limit > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 32; i++) g[i] = fminf(g[i], a.limit);
+  }
+  a.limit = ACT == MOE_ACT_SILU && GATED && a.limit > 0.f ? a.limit : INFINITY;
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; i++) {
-    float h = fp8_act(a, g[i], GATED);
-    if (GATED) h *= fp8_up(a, u[i]) + a.beta;
-    g[i] = f0 + i < N ? h : 0.f;
-    m = fmaxf(m, fabsf(g[i]));
+    float h = fp8_act(a, g[i], false);
+    if (GATED) h *= (ACT == MOE_ACT_SILU ? fminf(fmaxf(u[i], -a.limit), a.limit) : u[i]) + a.beta;
+    g[i] = h;
   }
+  if (f0 + 32 > N) {  // values past N are no features
+#pragma unroll
+    for (int i = 0; i < 32; i++) g[i] = f0 + i < N ? g[i] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i++) m = fmaxf(m, fabsf(g[i]));
   return m;
 }
 template <bool GATED>
@@ -294,12 +272,11 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t* bias, i
   }
 }
 
-template <int MODE, int ABOX, bool PAIR>
+template <int MODE, int ABOX>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmG, const Fp8GemmArgs p, const int stages) {
-  constexpr int STAGE_BYTES = stage_bytes(ABOX, PAIR), A_BYTES = ABOX * BK;
-  constexpr int BMT = PAIR ? 2 * BM : BM;   // rows per tile
+  constexpr int STAGE_BYTES = stage_bytes(ABOX), A_BYTES = ABOX * BK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Meta& meta = *reinterpret_cast<Meta*>(smem + stages * STAGE_BYTES);
@@ -308,8 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &meta.abort_flag;
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int rank = PAIR ? (int)cluster_ctarank() : 0;  // 0 issues the MMAs
-  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; s++) {
       mbar_init(&meta.full[s], 1);
@@ -317,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kQuarters; b++) {
       mbar_init(&meta.tfull[b], 1);
-      mbar_init(&meta.tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
+      mbar_init(&meta.tempty[b], kEpiWarps);
     }
     for (int s = 0; s < 2; s++) {
       mbar_init(&meta.sfull[s], 1);
@@ -331,20 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED) prefetch_tmap(&tmG);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(&meta.tmem_slot, TMEM_COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(&meta.tmem_slot, TMEM_COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc(&meta.tmem_slot, TMEM_COLS);
+    tmem_relinquish();
   }
   pdl_enter();
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
   for (int e = threadIdx.x; e < p.E; e += kThreads) row0[e] = p.cnt ? p.cnt[e] : p.R;
   tc_fence_before();
-  if (PAIR) cluster_sync();  // barriers and TMEM of both CTAs
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const int nt = (p.N + (MODE == FP8_GATED ? 127 : 255)) / (MODE == FP8_GATED ? 128 : 256);
   if (warp == 2) {
@@ -362,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int32_t first = (int32_t)min(rows_before + incl - c, (int64_t)p.R);
       const int32_t end = (int32_t)min(rows_before + incl, (int64_t)p.R);
-      const int32_t mt = (end - first + BMT - 1) / BMT * nt;
+      const int32_t mt = (end - first + BM - 1) / BM * nt;
       int32_t tincl = mt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -396,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      for (int u = worker; ok && u < total; u += workers) {
-        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
-        const int arow = t.row0 + t.m0 + BM * rank;
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit t = unit_of(p, row0, tiles, u, nkb);
+        const int arow = t.row0 + t.m0;
         for (int kb = t.kb0; kb < t.kb1; kb++) {
           if (!wait(empty + 8 * s, phase ^ 1, abort, p.status)) {
             ok = false;
@@ -407,35 +376,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* sa = smem + s * STAGE_BYTES;
           uint8_t* sb = sa + A_BYTES;
           const int k0 = kb * BK;
-          if constexpr (PAIR) {
-            // The even CTA arms its stage for the bytes of both; the odd CTA's may land
-            // first (the phase cannot complete before the arrival).
-            const uint32_t fb = mapa_shared(&meta.full[s], 0);
-            if (rank == 0) mbar_arrive_expect_tx(&meta.full[s], 2 * STAGE_BYTES);
-            tma_load_2d_pair(&tmA, fb, sa, k0, arow);
-            // the even CTA stages the first weight block (gate rows), the odd one the second
-            // (up): an MMA group takes 64 rows from each
-            if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
-              tma_load_3d_pair(rank == 0 ? &tmG : &tmB, fb, sb, k0, t.n_blk * 128, t.e);
-            else if (MODE == FP8_GATED)
-              tma_load_4d_pair(&tmB, fb, sb, k0, t.n_blk * 128, rank, t.e);
-            else
-              tma_load_3d_pair(&tmB, fb, sb, k0, t.n_blk * BNB + 128 * rank, t.e);
-          } else {
-            mbar_arrive_expect_tx(&meta.full[s], STAGE_BYTES);
-            tma_load_2d(&tmA, &meta.full[s], sa, k0, arow);
-            // rows in MMA order: 64 of the first weight block (gate), 64 of the second (up), ...
+          mbar_arrive_expect_tx(&meta.full[s], STAGE_BYTES);
+          tma_load_2d(&tmA, &meta.full[s], sa, k0, arow);
+          // rows in MMA order: 64 of the first weight block (gate), 64 of the second (up), ...
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
-              const int blk = g & 1, r = (g >> 1) * 64;
-              uint8_t* dst = sb + g * 64 * BK;
-              if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
-                tma_load_3d(blk ? &tmB : &tmG, &meta.full[s], dst, k0, t.n_blk * 128 + r, t.e);
-              else if (MODE == FP8_GATED)  // [E][2][N][K]
-                tma_load_4d(&tmB, &meta.full[s], dst, k0, t.n_blk * 128 + r, blk, t.e);
-              else
-                tma_load_3d(&tmB, &meta.full[s], dst, k0, t.n_blk * BNB + blk * 128 + r, t.e);
-            }
+          for (int g = 0; g < 4; g++) {
+            const int blk = g & 1, r = (g >> 1) * 64;
+            uint8_t* dst = sb + g * 64 * BK;
+            if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
+              tma_load_3d(blk ? &tmB : &tmG, &meta.full[s], dst, k0, t.n_blk * 128 + r, t.e);
+            else if (MODE == FP8_GATED)  // [E][2][N][K]
+              tma_load_4d(&tmB, &meta.full[s], dst, k0, t.n_blk * 128 + r, blk, t.e);
+            else
+              tma_load_3d(&tmB, &meta.full[s], dst, k0, t.n_blk * BNB + blk * 128 + r, t.e);
           }
           issued++;
           if (++s == stages) {
@@ -444,16 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every load issued has landed before the CTA may exit (the last `stages` of them);
-      // of a pair: has been consumed, which both CTAs' empty barriers see
+      // every load issued has landed before the CTA may exit (the last `stages` of them)
       const uint32_t n = issued < (uint32_t)stages ? issued : (uint32_t)stages;
-      const uint32_t landed = PAIR ? empty : full;
       for (uint32_t j = issued - n; j < issued; j++) {
         const uint64_t t0 = global_timer();
-        while (!try_wait(landed + 8 * (j % stages), (j / stages) & 1) && global_timer() - t0 < kTimeoutNs) {
+        while (!try_wait(full + 8 * (j % stages), (j / stages) & 1) && global_timer() - t0 < kTimeoutNs) {
         }
       }
-    } else if ((warp == 1 || warp == 3) && rank == 0 && elect_one()) {
+    } else if ((warp == 1 || warp == 3) && elect_one()) {
       // ---------------------------------------------------------- MMA issuers
       // Warp 1 takes the even blocks of K (quarters 0, 1), warp 3 the odd ones (2, 3): a
       // barrier answers after some hundred cycles on a busy SM, and one thread's waits for a
@@ -466,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = odd;
       uint32_t phase = 0, par = 1, n = 0;  // n: blocks of K so far
       bool ok = true;
-      for (int u = worker; ok && u < total; u += workers) {
-        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit t = unit_of(p, row0, tiles, u, nkb);
         const int len = t.kb1 - t.kb0;
         for (int i = (n ^ odd) & 1; i < len; i += 2) {
           // all three are asked before the first answer is awaited
@@ -483,17 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            // (the epilogue warps, of a pair the odd CTA's too, hand over tensor memory only,
-            // for which this fence is the acquire)
             tc_fence_after();
-            // rows 128 h .. of the stage's weights (of a pair: 64 h .. in each CTA)
-            const uint64_t bh = bd + (h * (PAIR ? 64 : 128) * BK) / 16;
+            const uint64_t bh = bd + h * (BNH * BK / 16);  // rows 128 h .. of the stage's weights
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; kk++) mma_f8<PAIR>(tmem_base + h * BNH, ad + 2 * kk, bh + 2 * kk, kk > 0);
-            commit<PAIR>(&meta.tfull[q0 + h]);
+            for (int kk = 0; kk < BK / 32; kk++) mma_f8(tmem_base + h * BNH, ad + 2 * kk, bh + 2 * kk, kk > 0);
+            mma_commit(&meta.tfull[q0 + h]);
           }
           if (!ok) break;
-          commit<PAIR>(&meta.empty[s]);
+          mma_commit(&meta.empty[s]);
           par ^= 1;
           if ((s += 2) >= stages) {
             s -= stages;
@@ -503,8 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         n += len;
       }
       // all issued MMAs complete before the tensor memory is released
-      if (PAIR) mma_commit_pair(&meta.drain, kEvenCta);
-      else mma_commit(&meta.drain);
+      mma_commit(&meta.drain);
       const uint64_t t0 = global_timer();
       while (!mbar_try_wait(&meta.drain, 0) && global_timer() - t0 < kTimeoutNs) {
       }
@@ -516,13 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool vec = p.as_kb == 1 && p.as_row % 4 == 0 && (reinterpret_cast<uintptr_t>(p.as) & 15u) == 0;
       uint32_t n = 0;  // blocks of K so far
       bool ok = true;
-      for (int u = worker; ok && u < total; u += workers) {
-        const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        const Unit t = unit_of(p, row0, tiles, u, nkb);
         const BlockScales w = block_scales<MODE>(p, t, nbn, nkb);
-        const int m0 = t.m0 + BM * rank + lane, kb1 = uniform(t.kb1);
-        const float* x[4];  // rows past the last: any
+        const int m0 = t.m0 + lane, kb1 = uniform(t.kb1);
+        int row[4];  // rows past the last: any
 #pragma unroll
-        for (int r = 0; r < 4; r++) x[r] = p.as + (int64_t)(t.row0 + min(m0 + 32 * r, t.rows - 1)) * p.as_row;
+        for (int r = 0; r < 4; r++) row[r] = t.row0 + min(m0 + 32 * r, t.rows - 1);
         for (int kb = uniform(t.kb0); ok && kb < kb1; kb += kLoad) {
           float xs[4][kLoad], wa[kLoad], wb[kLoad];
 #pragma unroll
@@ -534,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (vec && kb % 4 == 0 && kb + kLoad <= kb1) {
 #pragma unroll
             for (int r = 0; r < 4; r++) {
-              const float4 a = __ldg(reinterpret_cast<const float4*>(x[r] + kb));
+              const float4 a = __ldg(reinterpret_cast<const float4*>(p.as + row[r] * p.as_row + kb));
               xs[r][0] = a.x, xs[r][1] = a.y, xs[r][2] = a.z, xs[r][3] = a.w;
             }
           } else {
@@ -542,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kLoad; i++) {
               const int64_t k = (int64_t)min(kb + i, kb1 - 1) * p.as_kb;
 #pragma unroll
-              for (int r = 0; r < 4; r++) xs[r][i] = __ldg(x[r] + k);
+              for (int r = 0; r < 4; r++) xs[r][i] = __ldg(p.as + row[r] * p.as_row + k);
             }
           }
 #pragma unroll
@@ -572,18 +519,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int nkb = (p.K + BK - 1) / BK, nbn = (p.N + 127) / 128, units = uniform(tiles[p.E] * p.splits);
     const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
-    const int r_in_tile = q * 32 + lane;  // of the CTA's 128 rows
+    const int r_in_tile = q * 32 + lane;
     // The current block's quarters: columns half * 32 .. + 31 of the 64 of each weight block,
     // and their barriers; quarters 0, 1 and 2, 3 take turns by one address bit.
     uint32_t tq = meta.tmem_slot + ((uint32_t)(q * 32) << 16) + half * 32;
-    uint32_t fq = smem_u32(meta.tfull), eq = PAIR ? mapa_shared(meta.tempty, 0) : smem_u32(meta.tempty);
+    uint32_t fq = smem_u32(meta.tfull), eq = smem_u32(meta.tempty);
     const uint32_t sfull = smem_u32(meta.sfull), sempty = smem_u32(meta.sempty);
     const uint32_t srow = smem_u32(meta.scale) + r_in_tile * 8;
     uint32_t n = 0, sn = 0;  // blocks of K so far, and whose scales were read
-    auto drained = [&](uint32_t bar) {
-      if (PAIR) warp_arrive_cluster_relaxed(bar, lane);
-      else warp_arrive(bar, lane);
-    };
     // this row's two scale products of the next block (each block once, in order)
     auto next_scales = [&]() -> float2 {
       float2 f;
@@ -601,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // A wait that gives up does not leave the loop: both halves of a quadrant meet in
     // every unit, so they walk the same list to its end (the waits then return at once).
-    for (int u = worker; u < units; u += workers) {
-      const Unit t = unit_of<BMT>(p, row0, tiles, u, nkb);
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const Unit t = unit_of(p, row0, tiles, u, nkb);
       const int kb0 = uniform(t.kb0), kb1 = uniform(t.kb1);
-      const int m = uniform(t.m0) + BM * rank;
+      const int m = uniform(t.m0);
       const bool valid = m + r_in_tile < t.rows;
       const int64_t grow = (int64_t)t.row0 + m + r_in_tile;
       const bool live = m + q * 32 < uniform(t.rows);  // whole warp: some row of this quadrant exists
@@ -618,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             warp_wait(fq + 8 * h, (n >> 1) & 1, abort, p.status);
-            drained(eq + 8 * h);
+            warp_arrive(eq + 8 * h, lane);
           }
           tq ^= 2 * BNH;
           fq ^= 16;
@@ -651,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c == 1 && asked) ready = test_wait(nf, npar);
               } else {
                 tc_fence_before();
-                drained(eq + 8 * h);
+                warp_arrive(eq + 8 * h, lane);
                 if (asked && !__all_sync(0xffffffffu, ready)) warp_wait(nf, npar, abort, p.status);
                 tc_fence_after();
                 tmem_ld16(nt, v[0]);  // (after the last quarter: whatever the next holds, not used)
@@ -737,9 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < kGroups; b++) {
         const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + b;
         if (valid && grp < nbn) {
-          const float s = fp8_scale(fmaxf(meta.amax[b][0][r_in_tile], meta.amax[b][1][r_in_tile]));
-          const float inv = __frcp_rn(s);
-          if (half == 0) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s;
+          const Fp8Scale s = fp8_scale_of(fmaxf(meta.amax[b][0][r_in_tile], meta.amax[b][1][r_in_tile]));
+          if (half == 0) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s.s;
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             const int f0 = grp * 128 + row_of(h);
@@ -747,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; i += 16) {
               if (f0 + i < p.N) {  // N is a multiple of 16
                 const float* x = &acc[b][h * 32 + i];
-                const uint2 lo = fp8_round8(x, s, inv), hi = fp8_round8(x + 8, s, inv);
-                *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0 + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0 + i) =
+                    make_uint4(fp8_round4(x, s), fp8_round4(x + 4, s), fp8_round4(x + 8, s), fp8_round4(x + 12, s));
               }
             }
           }
@@ -760,12 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncwarp();
   tc_fence_before();
-  if (PAIR) cluster_sync();  // both CTAs done: MMAs drained, loads consumed, remote arrivals made
-  else __syncthreads();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    if (PAIR) tmem_dealloc_pair(meta.tmem_slot, TMEM_COLS);
-    else tmem_dealloc(meta.tmem_slot, TMEM_COLS);
+    tmem_dealloc(meta.tmem_slot, TMEM_COLS);
   }
 }
 
@@ -783,54 +723,15 @@ bool map_stack(CUtensorMap* m, const void* base, uint64_t K, uint64_t N, uint64_
   return map_bytes(m, base, 3, dims, strides, box);
 }
 
-// Pairs of CTAs that can be resident at once on the current device (cached per device).
-template <int MODE>
-int max_pairs(cudaLaunchConfig_t cfg, int num_sms) {
-  static std::atomic<int> cache[64] = {};  // callers may race: each writes the same value
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
-  const int cached = cache[dev].load(std::memory_order_relaxed);
-  if (cached > 0) return cached;
-  int n = 0;
-  cfg.gridDim = dim3(2 * (unsigned)(num_sms / 2), 1, 1);
-  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<MODE, 128, true>, &cfg) != cudaSuccess || n <= 0) {
-    (void)cudaGetLastError();
-    n = num_sms / 2;
-  }
-  cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-template <int MODE, int ABOX, bool PAIR>
+template <int MODE, int ABOX>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& g, const Fp8GemmArgs& p, cudaStream_t st) {
-  const int stages = stages_for(ABOX, PAIR, p.E);
-  const int smem = 1024 + stages * stage_bytes(ABOX, PAIR) + meta_bytes(p.E);
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int stages = stages_for(ABOX, p.E);
+  const int smem = 1024 + stages * stage_bytes(ABOX) + meta_bytes(p.E);
+  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (PAIR) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 2;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    n++;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
   const int64_t units = (int64_t)p.max_tiles * p.splits;
-  int64_t most = p.num_sms;
-  if constexpr (PAIR) most = max_pairs<MODE>(cfg, p.num_sms);
-  cfg.gridDim = dim3((PAIR ? 2 : 1) * (unsigned)(units < most ? units : most), 1, 1);
-  if (pdl_enabled()) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = n + 1;
-  }
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<MODE, ABOX, PAIR>, a, b, g, p, stages);
+  const unsigned grid = (unsigned)(units < p.num_sms ? units : p.num_sms);
+  return launch_pdl(fp8_gemm_kernel<MODE, ABOX>, grid, kThreads, smem, st, a, b, g, p, stages);
 }
 
 template <int MODE>
@@ -838,7 +739,7 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
   // no group has more than R rows: small batches load a shorter row tile and leave room
   // for more weight stages (the accumulator rows past it are never stored)
   const uint32_t abox = p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
-  const uint32_t brows = p.pair ? 128 : 64;  // weight rows per box
+  constexpr uint32_t brows = 64;  // weight rows per box
   CUtensorMap a, b, g;
   const uint64_t dims[2] = {(uint64_t)p.K, (uint64_t)p.R};
   const uint64_t strides[1] = {(uint64_t)p.K};
@@ -858,10 +759,9 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
     g = b;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (p.pair) return launch<MODE, 128, true>(a, b, g, p, st);
-  if (abox == 32) return launch<MODE, 32, false>(a, b, g, p, st);
-  if (abox == 64) return launch<MODE, 64, false>(a, b, g, p, st);
-  return launch<MODE, 128, false>(a, b, g, p, st);
+  if (abox == 32) return launch<MODE, 32>(a, b, g, p, st);
+  if (abox == 64) return launch<MODE, 64>(a, b, g, p, st);
+  return launch<MODE, 128>(a, b, g, p, st);
 }
 
 }  // namespace
@@ -869,13 +769,6 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms) {
   if (R > kSplitMaxRows) return 1;
   return choose_splits(fp8_m_tiles(R, E) * fp8_n_tiles(mode, N), (int)((K + BK - 1) / BK), sms);
-}
-
-bool fp8_pair(int64_t R, int64_t E) {
-  const char* env = std::getenv("MOE_B200_PAIR_FP8");
-  if (env && env[0] == '0') return false;
-  if (env && env[0] == '1') return R > 64;
-  return R > kSplitMaxRows && R >= 512 * E;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, cudaStream_t st) {

@@ -137,8 +137,7 @@ __device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& r
   } else {
 #pragma unroll
     for (int n = 0; n < L::N; n++) {
-      float r;
-      sigmoid_pair(l[n], &s[n], &r);
+      s[n] = fast_rcp(1.f + fast_exp(-l[n]));  // 0 from -87 down
       sum += s[n];
     }
   }
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(RouterTrainArgs a)
 constexpr int kBackThreads = 256;
 
 template <class L>
-__global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTrainArgs a) {
+__global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backward_kernel(RouterTrainArgs a) {
   constexpr int G = L::G, N = L::N, V = L::V;
   constexpr int kSlots = N < 32 / G ? N : 32 / G;  // slots per lane: k <= E, k <= 32
   constexpr int groups = kBackThreads / G;
@@ -415,6 +414,7 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
     // routing: the slots' scores (softmax) or logits (sigmoid) through the row in shared
     // memory, and their sums
     float kept = 0.f, dot = 0.f, ss[kSlots], sr[kSlots];
+    bool twice[kSlots];
     if (a.dw) {
       store_row(soft ? s : l);
       __syncwarp();
@@ -431,6 +431,16 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
       }
       kept = group_sum<G>(kept);
       dot = group_sum<G>(dot);
+      // does another lane's slot name the same expert?  Each leaves its number there.
+#pragma unroll
+      for (int q = 0; q < kSlots; q++) {
+        twice[q] = false;
+        if (q > 0 && q * G >= a.k) break;
+        __syncwarp();
+        if (slots.e[q] >= 0) reinterpret_cast<int*>(mine)[slots.e[q]] = lane;
+        __syncwarp();
+        if (slots.e[q] >= 0) twice[q] = reinterpret_cast<int*>(mine)[slots.e[q]] != lane;
+      }
       __syncwarp();
     }
     // w_j = S s_j / den: ds_j = S / den (dw_j - [not clamped] dot / den)
@@ -461,15 +471,14 @@ __global__ void __launch_bounds__(kBackThreads) router_backward_kernel(RouterTra
     }
     if (a.dw) {
       store_row(d);
+      __syncwarp();
 #pragma unroll
       for (int q = 0; q < kSlots; q++) {
         if (q > 0 && q * G >= a.k) break;
         const int e = slots.e[q];
         const float add = f * (slots.dw[q] - shift) * ss[q] * sr[q];
         // slots of one token that name the same expert are added in slot order
-        const unsigned same = __match_any_sync(0xffffffffu, e >= 0 ? (group % 32) * a.E + e : -1 - (int)(threadIdx.x & 31));
-        __syncwarp();
-        if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+        if (__any_sync(0xffffffffu, twice[q])) {
           for (int g = 0; g < G; g++) {
             if (lane == g && e >= 0) mine[e] += add;
             __syncwarp();
@@ -533,10 +542,10 @@ struct Partial {
 template <class L>
 struct Backward {
   static cudaError_t go(const RouterTrainArgs& a, int sms, cudaStream_t st) {
-    // neighbouring tokens to a block, whole steps of its groups, eight blocks per SM at most
+    // neighbouring tokens to a block, whole steps of its groups, four blocks per SM at most
     constexpr int groups = kBackThreads / L::G;
     RouterTrainArgs b = a;
-    const int64_t per = ((int64_t)a.T + (int64_t)sms * 8 - 1) / ((int64_t)sms * 8);
+    const int64_t per = ((int64_t)a.T + (int64_t)sms * 4 - 1) / ((int64_t)sms * 4);
     b.chunk = (int)((per + groups - 1) / groups * groups);
     return launch_pdl(router_backward_kernel<L>, (unsigned)((a.T + b.chunk - 1) / b.chunk), kBackThreads,
                       (size_t)kBackThreads * L::N * 4, st, b);

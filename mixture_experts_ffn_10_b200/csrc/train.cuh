@@ -5,7 +5,7 @@
 
 namespace moe {
 
-constexpr int kBalanceMaxChunks = 592;  // blocks of tokens of the balance loss (four per SM)
+constexpr int kBalanceMaxChunks = 444;  // blocks of tokens of the balance loss (three per SM: one wave)
 
 struct RouterTrainArgs {
   const void* logits;        // [T, E]

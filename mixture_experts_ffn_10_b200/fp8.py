@@ -22,6 +22,7 @@ import mixture_experts_ffn_10_b200 as _m
 EXPORTED = ("moe_fp8_quantize", "moe_fp8_quantize_weights", "moe_fp8_matmul_workspace_size", "moe_fp8_matmul")
 BLOCK = 128
 
+_NOTHING = contextlib.nullcontext()
 _lib = None
 
 
@@ -46,7 +47,7 @@ def _on(device):
     if device.type != "cuda":
         raise ValueError(f"expected tensors on a CUDA device, got {device}")
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _NOTHING
     return torch.cuda.device(device)
 
 
@@ -109,7 +110,7 @@ def quantize_gate_up(w, stream=None):
 
 
 def _operand(name, t, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} "
                          f"on {t.device}")
 

@@ -17,6 +17,7 @@ configuration (T, E, k, score, renormalize, routed_scale, logit_dtype, ...).
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import types
 
 import torch
@@ -28,10 +29,12 @@ from .fp8 import _on, _operand, _stream
 EXPORTED = ("moe_balance_workspace_size", "moe_balance_loss", "moe_router_backward")
 
 _lib = None
-_structs: dict = {}
+_structs: dict = {}  # ctypes structures by the values of a configuration
+_sizes: dict = {}    # workspace bytes by (T, E, B)
 
 _FIELDS = ("T", "d", "F", "E", "k", "Fs", "act_dtype", "w_dtype", "logit_dtype", "score", "renormalize", "routed_scale",
            "n_group", "topk_group", "weigh_inputs", "act", "alpha", "beta", "limit", "gu_layout", "shared_gate")
+_VALUES = operator.attrgetter(*_FIELDS)
 
 
 def _library():
@@ -51,7 +54,7 @@ def _library():
 
 def _config(cfg):
     """(shape, options) of a configuration, made once per set of values."""
-    key = (*(getattr(cfg, n) for n in _FIELDS), getattr(cfg, "ffn", "gated"))
+    key = (*_VALUES(cfg), getattr(cfg, "ffn", "gated"))
     got = _structs.get(key)
     if got is None:
         if len(_structs) > 256:
@@ -92,7 +95,13 @@ def balance_loss(cfg, logits, idx, coef=1.0, seq_offsets=None, router_bias=None,
         counts = torch.empty((B, cfg.E), dtype=torch.int32, device=dev)
         loss = torch.empty((), dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = _m.Workspace(lib.moe_balance_workspace_size(shape, opts, B), dev)
+            key = (cfg.T, cfg.E, B)  # what the size depends on
+            nbytes = _sizes.get(key)
+            if nbytes is None:
+                if len(_sizes) > 256:
+                    _sizes.clear()
+                nbytes = _sizes[key] = lib.moe_balance_workspace_size(shape, opts, B)
+            workspace = _m.Workspace(nbytes, dev)
         _m._check(lib.moe_balance_loss(shape, opts, logits.data_ptr(), _ptr(router_bias), idx.data_ptr(), _ptr(seq_offsets), B,
                                        coef, counts.data_ptr(), loss.data_ptr(), workspace.ptr, workspace.nbytes,
                                        _stream(stream, dev)))
