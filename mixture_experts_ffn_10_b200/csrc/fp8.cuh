@@ -103,6 +103,37 @@ __device__ __forceinline__ uint32_t fp8_round4(const float* x, const Fp8Scale& f
                    fp8_quotient(x[3], f.s, f.hi));
 }
 
+// Rounding bf16 values, whose block's largest magnitude is a bf16 value (or the floor
+// 2^-100): no bracket is needed.  With eight-bit significands p of x and a of amax, 448 x /
+// amax = 7 p 2^i / a equals a halfway point odd 2^j (odd < 32) or differs from it by 1 / (31 *
+// 255) > 2^-13 relative at least.  And x / s differs from 448 x / amax by the rounding of s
+// alone, a common factor 1 - d, |d| <= 2^-24: if s was rounded, every tie of the block falls to
+// the same side, which a factor 1 +- 2^-16 on the quotients decides without touching any
+// other value; if s is exact, ties go to the even value, for which the quotient itself has
+// to be: x inv, corrected by its remainder.  (Such ties are one value in two hundred of
+// normal data, one warp in two meets some.)
+struct Fp8ScaleBf16 {
+  float s, inv, fix;  // fix: factor of the remainder's correction, 0 where none is due
+};
+__device__ __forceinline__ Fp8ScaleBf16 fp8_scale_of_bf16(float amax) {
+  const float s = fp8_scale(amax), inv = __fdividef(1.f, s);
+  const float rem = fmaf(-448.f, s, fmaxf(amax, 0x1p-100f));  // exact; > 0: s was rounded down
+  if (rem == 0.f) return Fp8ScaleBf16{s, inv, inv};
+  return Fp8ScaleBf16{s, inv * (rem > 0.f ? 1.f + 0x1p-16f : 1.f - 0x1p-16f), 0.f};
+}
+// Whole warp (lanes may hold different blocks): 16 values.
+__device__ __forceinline__ void fp8_round16_bf16(const float (&x)[16], const Fp8ScaleBf16& f, uint32_t (&w)[4]) {
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) t[i] = x[i] * f.inv;
+  if (__any_sync(0xffffffffu, f.fix != 0.f)) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) t[i] = fmaf(-fmaf(t[i], f.s, -x[i]), f.fix, t[i]);  // (keeps -0)
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] = fp8_pack4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+}
+
 // ---------------------------------------------------------------- activation
 // act(g) in fp32 (h is rounded to e4m3 next to it, a step of 2^-4: the hardware tanh of the
 // bf16 epilogues, 5e-4 off, would move too many values over a rounding border); the SiLU

@@ -61,13 +61,26 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
-// The lane's 16 values rounded, to q (its first column's place): whole, or (rows of a
+// The lane's 16 values rounded under the block's largest magnitude; returns the scale.
+// Whole warp.
+template <bool BF16>
+__device__ __forceinline__ float round16(const float (&f)[16], float amax, uint32_t (&w)[4]) {
+  if constexpr (BF16) {
+    const Fp8ScaleBf16 s = fp8_scale_of_bf16(amax);
+    fp8_round16_bf16(f, s, w);
+    return s.s;
+  } else {
+    const Fp8Scale s = fp8_scale_of(amax);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = fp8_round4(f + 4 * i, s);
+    return s.s;
+  }
+}
+
+// Sixteen rounded values to q (the lane's first column's place): whole, or (rows of a
 // multiple of 8 or 4 values) the vectors below K.
 template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void store16(uint8_t* q, int col, int K, const float (&f)[16], const Fp8Scale& s) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) w[i] = fp8_round4(f + 4 * i, s);
+__device__ __forceinline__ void store16(uint8_t* q, int col, int K, const uint32_t (&w)[4]) {
   if constexpr (WHOLE) {
     if (col < K) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
   } else if constexpr (BF16) {
@@ -81,9 +94,9 @@ __device__ __forceinline__ void store16(uint8_t* q, int col, int K, const float 
 }
 
 // Rows in vectors: eight lanes per block of 128 columns, so that a block's maximum and
-// scale are worked out by eight lanes for 16 values each; two blocks in flight.  With eight
-// values per lane the kernel was bound by instructions (183 per eight values, 16384 rows of
-// 7168: 113 us).
+// scale are worked out by eight lanes for 16 values each; two blocks in flight.  Bound by
+// instructions at first (183 per eight values with the test of every value for a near tie
+// and eight values per lane: 16384 rows of 7168 took 113 us, 54 at the memory's rate).
 constexpr int kLanes = 8, kGroups = kThreads / kLanes, kBatch = 2;
 template <bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const uint8_t* x, int64_t pitch_bytes, int K, int nb,
@@ -117,10 +130,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const uint8_t* 
     const int64_t b = b0 + i * kGroups;
     float f[16];
     v[i].unpack(f);
-    const Fp8Scale s = fp8_scale_of(lanes_max<kLanes>(amax16(f)));
+    uint32_t w[4];
+    const float s = round16<BF16>(f, lanes_max<kLanes>(amax16(f)), w);
     if (b < blocks) {
-      store16<BF16, WHOLE>(q + row[i] * K + col[i], col[i], K, f, s);
-      if (lane == 0) scales[b] = s.s;
+      store16<BF16, WHOLE>(q + row[i] * K + col[i], col[i], K, w);
+      if (lane == 0) scales[b] = s;
     }
   }
 }
@@ -182,15 +196,17 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_kernel(const uint8_
   m = warp_max[0];
 #pragma unroll
   for (int i = 1; i < kThreads / 32; i++) m = fmaxf(m, warp_max[i]);
-  const Fp8Scale s = fp8_scale_of(m);
+  float s = 0.f;
 #pragma unroll
   for (int i = 0; i < kIter; i++) {
     const int64_t n = n0 + r0 + i * kGroups;
     float f[16];
+    uint32_t o[4];
     v[i].unpack(f);
-    if (n < N) store16<BF16, WHOLE>(q + (e * N + n) * K + col, col, (int)K, f, s);
+    s = round16<BF16>(f, m, o);
+    if (n < N) store16<BF16, WHOLE>(q + (e * N + n) * K + col, col, (int)K, o);
   }
-  if (threadIdx.x == 0) scales[blk] = s.s;
+  if (threadIdx.x == 0) scales[blk] = s;
 }
 
 // The same for rows of any size and alignment, reading the block twice.
@@ -251,13 +267,10 @@ __global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs
     float f[16];
     v[i].unpack(f);
     const float m = lanes_max<kLanes>(amax16(f));
-    if (tok[i] >= a.T) continue;
-    Fp8Scale s = fp8_scale_of(m);
     uint32_t w[4] = {};
-    if (!a.weigh_inputs) {
-#pragma unroll
-      for (int c = 0; c < 4; c++) w[c] = fp8_round4(f + 4 * c, s);
-    }
+    float s = 0.f;
+    if (!a.weigh_inputs) s = round16<true>(f, m, w);
+    if (tok[i] >= a.T) continue;
     for (int j = 0; j < a.k; j++) {
       const int row = a.pos[(int64_t)tok[i] * a.k + j];
       if (row < 0 || row >= a.R) {
@@ -270,13 +283,11 @@ __global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs
         float g[16];
 #pragma unroll
         for (int c = 0; c < 16; c++) g[c] = f[c] * wt;
-        s = fp8_scale_of(fabsf(m * wt));
-#pragma unroll
-        for (int c = 0; c < 4; c++) w[c] = fp8_round4(g + 4 * c, s);
+        s = round16<false>(g, fabsf(m * wt), w);
       }
       // d is a multiple of 16
       if (col < a.d) *reinterpret_cast<uint4*>(a.xq + (int64_t)row * a.d + col) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (lane == 0) a.xs[(int64_t)at[i] * a.R + row] = s.s;
+      if (lane == 0) a.xs[(int64_t)at[i] * a.R + row] = s;
     }
   }
 }

@@ -81,12 +81,13 @@ def test_quantize_ties_and_borders(fp8, dtype):
 
 
 def test_quantize_every_bf16_ratio(fp8):
-    """Every bf16 mantissa as a value under every bf16 mantissa as the block's maximum, over 14 binades:
-    all the exact ties that bf16 inputs can meet."""
+    """Every bf16 mantissa as a value under every bf16 mantissa as the block's maximum, over 21 binades
+    (down to what rounds to zero), for maxima of three sizes: all the exact ties that bf16 inputs can meet."""
     sig = torch.arange(128, 256, device="cuda", dtype=torch.float32)
-    x = torch.empty((128, 14, 1, 128), device="cuda")
-    x[:] = sig[None, None, None, :] * torch.exp2(-torch.arange(1, 15, device="cuda").float())[None, :, None, None]
-    x = torch.cat((x, sig[:, None, None, None].expand(128, 14, 1, 1)), 3)  # 129 values: the maximum goes to its own place
+    x = torch.empty((128, 21, 1, 128), device="cuda")
+    x[:] = sig[None, None, None, :] * torch.exp2(-torch.arange(1, 22, device="cuda").float())[None, :, None, None]
+    x = torch.cat((x, sig[:, None, None, None].expand(128, 21, 1, 1)), 3)  # 129 values: the maximum goes to its own place
+    x = torch.cat((x, x * 2.0 ** 60, x * 2.0 ** -70))
     x = torch.cat((x[..., 128:], x[..., 1:128]), 3).reshape(-1, 128).to(torch.bfloat16)
     q, s = fp8.quantize(x)
     rq, rs = quantize_ref(x)
