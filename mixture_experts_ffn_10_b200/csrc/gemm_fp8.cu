@@ -84,6 +84,15 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Waits for the thread's TMEM loads; r is in place after it (and not read before).
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -208,35 +217,28 @@ __device__ __forceinline__ BlockScales block_scales(const Fp8GemmArgs& p, const 
   return b;
 }
 
-// Features f0 .. f0 + 31 of a row: gate (or plain) sums in g, up sums in u -> activated
-// values in g; returns their largest magnitude.  One activation per instance, so that the
-// 32 unrolled values run a short straight piece of code.
+// Features f0 .. f0 + 15 of a row: gate (or plain) sums in g, up sums in u -> activated
+// values in g; returns their largest magnitude.  One activation per instance: the values
+// run a short straight piece of code.
 template <bool GATED, int ACT>
-__device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], const ActParams& act, int f0, int N) {
-  ActParams a = act;
+__device__ __forceinline__ float activate(float (&g)[16], const float (&u)[16], ActParams a, int f0, int N) {
   a.act = ACT;
   if (ACT == MOE_ACT_SILU && GATED && a.limit > 0.f) {
 #pragma unroll
-    for (int i = 0; i < 32; i++) g[i] = fminf(g[i], a.limit);
+    for (int i = 0; i < 16; i++) g[i] = fminf(g[i], a.limit);
   }
   a.limit = ACT == MOE_ACT_SILU && GATED && a.limit > 0.f ? a.limit : INFINITY;
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; i++) {
-    float h = fp8_act(a, g[i], false);
-    if (GATED) h *= (ACT == MOE_ACT_SILU ? fminf(fmaxf(u[i], -a.limit), a.limit) : u[i]) + a.beta;
-    g[i] = h;
+  for (int i = 0; i < 16; i++) {
+    g[i] = fp8_act(a, g[i], false);
+    if (GATED) g[i] *= (ACT == MOE_ACT_SILU ? fminf(fmaxf(u[i], -a.limit), a.limit) : u[i]) + a.beta;
+    m = fmaxf(m, fabsf(g[i]));
   }
-  if (f0 + 32 > N) {  // values past N are no features
-#pragma unroll
-    for (int i = 0; i < 32; i++) g[i] = f0 + i < N ? g[i] : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 32; i++) m = fmaxf(m, fabsf(g[i]));
-  return m;
+  return f0 < N ? m : 0.f;  // N is a multiple of 16
 }
 template <bool GATED>
-__device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], const ActParams& act, int f0, int N) {
+__device__ __forceinline__ float activate(float (&g)[16], const float (&u)[16], const ActParams& act, int f0, int N) {
   switch (act.act) {
     case MOE_ACT_SILU: return activate<GATED, MOE_ACT_SILU>(g, u, act, f0, N);
     case MOE_ACT_GELU_ERF: return activate<GATED, MOE_ACT_GELU_ERF>(g, u, act, f0, N);
@@ -247,29 +249,10 @@ __device__ __forceinline__ float activate(float (&g)[32], const float (&u)[32], 
 }
 
 // v[i] += bias[c0 + i] for the columns below N (a multiple of 8).
-__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t* bias, int c0, int N) {
-  const bool vec = (reinterpret_cast<uintptr_t>(bias + c0) & 15u) == 0;
+__device__ __forceinline__ void add_bias(float (&v)[16], const uint16_t* bias, int c0, int N) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    if (c0 + i < N) {
-      uint4 q;
-      if (vec) {
-        q = __ldg(reinterpret_cast<const uint4*>(bias + c0 + i));
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-          w[c] = __ldg(bias + c0 + i + 2 * c) | ((uint32_t)__ldg(bias + c0 + i + 2 * c + 1) << 16);
-        q = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int c = 0; c < 4; c++) {
-        v[i + 2 * c] += bf16_to_f32(w[c] & 0xffff);
-        v[i + 2 * c + 1] += bf16_to_f32(w[c] >> 16);
-      }
-    }
-  }
+  for (int i = 0; i < 16; i++)
+    if (c0 + i < N) v[i] += bf16_to_f32(__ldg(bias + c0 + i));
 }
 
 template <int MODE, int ABOX>
@@ -594,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c == 1 && asked) ready = test_wait(nf, npar);
               } else {
                 tc_fence_before();
-                warp_arrive(eq + 8 * h, lane);
+                if (left > 1) warp_arrive(eq + 8 * h, lane);  // the last block's quarters are kept
                 if (asked && !__all_sync(0xffffffffu, ready)) warp_wait(nf, npar, abort, p.status);
                 tc_fence_after();
                 tmem_ld16(nt, v[0]);  // (after the last quarter: whatever the next holds, not used)
@@ -611,90 +594,115 @@ __global__ void __launch_bounds__(kThreads, 1)
           eq ^= 16;
         }
         tmem_ld_wait16(v[0]);
+        // The sums go back to tensor memory, to this thread's columns of the quarters kept, for
+        // the loops below to walk: unrolled over registers, what follows was some 2500
+        // instructions, 6 to 17 thousand cycles for a tile, most of them waiting for code.
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          tmem_st16((tq ^ (2 * BNH)) + (i >> 1 & 1) * BNH + (i >> 2) * 64 + (i & 1) * 16, &acc[i >> 2][(i & 3) * 16]);
+        tmem_st_wait();
       }
 
-      // acc[b][32 h ..] starts at row (column of the output) row_of(h) of weight block b
-      auto row_of = [&](int h) { return h * 64 + half * 32; };
+      // Run c of 16 columns, c < 4: weight block 0, c < 8: block 1; its place in tensor memory
+      // and its first row within the block.
+      const uint32_t tl = tq ^ (2 * BNH), el = eq ^ 16;
+      auto place = [&](int c) { return tl + (c >> 1 & 1) * BNH + (c >> 2) * 64 + (c & 1) * 16; };
+      auto first_row = [&](int c) { return (c >> 1 & 1) * 64 + half * 32 + (c & 1) * 16; };
+      auto fetch = [&](int c, float (&v)[16]) {
+        uint32_t r[16];
+        tmem_ld16(place(c), r);
+        tmem_ld_wait16(r);
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+      };
+      auto give_back = [&]() {
+        tc_fence_before();
+        warp_arrive(el, lane);
+        warp_arrive(el + 8, lane);
+      };
       if (p.splits > 1) {
-        if (valid) {
+        if (live) {
+          float* out = p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB;
+#pragma unroll 1
+          for (int c = 0; c < 8; c++) {
+            float v[16];
+            fetch(c, v);
+            if (valid) {
+              float4* o = reinterpret_cast<float4*>(out + (c >> 2) * 128 + first_row(c));
 #pragma unroll
-          for (int b = 0; b < 2; b++) {
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              float4* out = reinterpret_cast<float4*>(p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB +
-                                                      b * 128 + row_of(h));
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                out[i / 4] = make_float4(acc[b][h * 32 + i], acc[b][h * 32 + i + 1], acc[b][h * 32 + i + 2], acc[b][h * 32 + i + 3]);
+              for (int i = 0; i < 4; i++) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
+          give_back();
         }
         continue;
       }
       if (MODE == FP8_LINEAR) {
-        if (valid) {
-          const float w = p.roww ? p.roww[grow] : 1.f;
-          const int64_t orow = p.y_row ? p.y_row[grow] : grow;
+        if (live) {
+          const float w = p.roww && valid ? p.roww[grow] : 1.f;
+          const int64_t orow = p.y_row && valid ? p.y_row[grow] : grow;
+          const uint16_t* bias = p.bias ? p.bias + (int64_t)t.e * p.N : nullptr;
+#pragma unroll 1
+          for (int c = 0; c < 8; c++) {
+            float v[16];
+            fetch(c, v);
+            const int n0 = t.n_blk * BNB + (c >> 2) * 128 + first_row(c);
+            if (bias) add_bias(v, bias, n0, p.N);
+            uint16_t* out = p.y + orow * p.N + n0;
 #pragma unroll
-          for (int b = 0; b < 2; b++) {
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              float (&v)[32] = *reinterpret_cast<float (*)[32]>(&acc[b][h * 32]);
-              const int n0 = t.n_blk * BNB + b * 128 + row_of(h);
-              if (p.bias) add_bias(v, p.bias + (int64_t)t.e * p.N, n0, p.N);
-              uint16_t* out = p.y + orow * p.N + n0;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                if (n0 + i < p.N)  // N is a multiple of 8
-                  *reinterpret_cast<uint4*>(out + i) =
-                      make_uint4(pack_bf16x2(v[i] * w, v[i + 1] * w), pack_bf16x2(v[i + 2] * w, v[i + 3] * w),
-                                 pack_bf16x2(v[i + 4] * w, v[i + 5] * w), pack_bf16x2(v[i + 6] * w, v[i + 7] * w));
-              }
+            for (int i = 0; i < 16; i += 8) {
+              if (valid && n0 + i < p.N)  // N is a multiple of 8
+                *reinterpret_cast<uint4*>(out + i) =
+                    make_uint4(pack_bf16x2(v[i] * w, v[i + 1] * w), pack_bf16x2(v[i + 2] * w, v[i + 3] * w),
+                               pack_bf16x2(v[i + 4] * w, v[i + 5] * w), pack_bf16x2(v[i + 6] * w, v[i + 7] * w));
             }
           }
+          give_back();
         }
         continue;
       }
-      // gated / plain: activate, agree on each row's largest magnitude per 128 features,
-      // round.  Gated: one group per tile (block 0 gate, block 1 up); plain: two.
-      constexpr int kGroups = MODE == FP8_GATED ? 1 : 2;
+      // gated / plain: activate (back into tensor memory), agree on each row's largest
+      // magnitude per 128 features, round.  Gated: one group per tile (block 0 gate, block 1
+      // up); plain: two.
+      constexpr int kRuns = MODE == FP8_GATED ? 4 : 8;  // of 16 features
       if (live) {
         const Fp8Bias bias = fp8_bias(MODE, p.layout, t.e, p.N, p.bias, p.gate_bias);
-#pragma unroll
-        for (int b = 0; b < kGroups; b++) {
-          float m = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            float (&g)[32] = *reinterpret_cast<float (*)[32]>(&acc[b][h * 32]);
-            float (&u)[32] = *reinterpret_cast<float (*)[32]>(&acc[1][h * 32]);
-            const int f0 = (MODE == FP8_GATED ? t.n_blk * 128 : t.n_blk * BNB + b * 128) + row_of(h);
-            if (bias.g) add_bias(g, bias.g, f0, p.N);
-            if (bias.u) add_bias(u, bias.u, f0, p.N);
-            m = fmaxf(m, activate<MODE == FP8_GATED>(g, u, p.act, f0, p.N));
+        float m = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < kRuns; c++) {
+          float g[16], u[16];
+          fetch(c, g);
+          if (MODE == FP8_GATED) fetch(c + 4, u);
+          const int f0 = (MODE == FP8_GATED ? t.n_blk * 128 : t.n_blk * BNB + (c >> 2) * 128) + first_row(c);
+          if (bias.g) add_bias(g, bias.g, f0, p.N);
+          if (bias.u) add_bias(u, bias.u, f0, p.N);
+          m = fmaxf(m, activate<MODE == FP8_GATED>(g, u, p.act, f0, p.N));
+          tmem_st16(place(c), g);
+          if ((c & 3) == 3) {
+            meta.amax[c >> 2][half][r_in_tile] = m;
+            m = 0.f;
           }
-          meta.amax[b][half][r_in_tile] = m;
         }
+        tmem_st_wait();
       }
       quadrant_sync(q);
-#pragma unroll
-      for (int b = 0; b < kGroups; b++) {
-        const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + b;
-        if (valid && grp < nbn) {
-          const Fp8Scale s = fp8_scale_of(fmaxf(meta.amax[b][0][r_in_tile], meta.amax[b][1][r_in_tile]));
-          if (half == 0) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s.s;
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const int f0 = grp * 128 + row_of(h);
-#pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-              if (f0 + i < p.N) {  // N is a multiple of 16
-                const float* x = &acc[b][h * 32 + i];
-                *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0 + i) =
-                    make_uint4(fp8_round4(x, s), fp8_round4(x + 4, s), fp8_round4(x + 8, s), fp8_round4(x + 12, s));
-              }
-            }
+      if (live) {
+        Fp8Scale s{};
+#pragma unroll 1
+        for (int c = 0; c < kRuns; c++) {
+          const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + (c >> 2);
+          if ((c & 3) == 0) {
+            s = fp8_scale_of(fmaxf(meta.amax[c >> 2][0][r_in_tile], meta.amax[c >> 2][1][r_in_tile]));
+            if (valid && half == 0 && grp < nbn) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s.s;
           }
+          float h[16];
+          fetch(c, h);
+          const int f0 = grp * 128 + first_row(c);
+          if (valid && f0 < p.N)  // N is a multiple of 16
+            *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0) =
+                make_uint4(fp8_round4(h, s), fp8_round4(h + 4, s), fp8_round4(h + 8, s), fp8_round4(h + 12, s));
         }
+        give_back();
       }
       quadrant_sync(q);  // the maxima are read before the next tile's are written
     }
