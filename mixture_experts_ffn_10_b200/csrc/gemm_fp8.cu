@@ -11,8 +11,8 @@
 // and the accumulators live in its registers for the whole K loop.  (With the weights as M
 // the row scales would differ from register to register and each multiply-add would need
 // an operand from shared memory.)  Tensor memory is a ring of four quarters of 128 columns;
-// a block of K is two MMA groups of N = 128 (64 rows of each weight block), each handed
-// over by itself, so that the adds of one quarter run beside the products of the others:
+// a block of K is two MMA groups of N = 128 (one per weight block), each handed over by
+// itself, so that the adds of one quarter run beside the products of the others:
 // with two halves of 256 columns the chain product - hand-over - adds - hand-over of a
 // buffer was longer than two products.
 //
@@ -41,7 +41,7 @@ using namespace sm100;
 constexpr int BM = kFp8BM;
 constexpr int BK = kFp8Block;     // bytes of K per stage: one scale block
 constexpr int BNB = 256;          // weight rows per tile
-constexpr int BNH = 128;          // of them per MMA group: 64 of each of the tile's two weight blocks
+constexpr int BNH = 128;          // of them per MMA group: one of the tile's two weight blocks
 constexpr int kQuarters = 4;      // accumulators of BNH columns in tensor memory
 constexpr int TMEM_COLS = kQuarters * BNH;
 constexpr int kEpiWarps = 8;
@@ -361,17 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k0 = kb * BK;
           mbar_arrive_expect_tx(&meta.full[s], STAGE_BYTES);
           tma_load_2d(&tmA, &meta.full[s], sa, k0, arow);
-          // rows in MMA order: 64 of the first weight block (gate), 64 of the second (up), ...
-#pragma unroll
-          for (int g = 0; g < 4; g++) {
-            const int blk = g & 1, r = (g >> 1) * 64;
-            uint8_t* dst = sb + g * 64 * BK;
-            if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED)
-              tma_load_3d(blk ? &tmB : &tmG, &meta.full[s], dst, k0, t.n_blk * 128 + r, t.e);
-            else if (MODE == FP8_GATED)  // [E][2][N][K]
-              tma_load_4d(&tmB, &meta.full[s], dst, k0, t.n_blk * 128 + r, blk, t.e);
-            else
-              tma_load_3d(&tmB, &meta.full[s], dst, k0, t.n_blk * BNB + blk * 128 + r, t.e);
+          if (MODE == FP8_GATED && p.layout == MOE_GU_UNFUSED) {
+            tma_load_3d(&tmG, &meta.full[s], sb, k0, t.n_blk * 128, t.e);
+            tma_load_3d(&tmB, &meta.full[s], sb + BNH * BK, k0, t.n_blk * 128, t.e);
+          } else if (MODE == FP8_GATED) {  // [E][2][N][K]: gate rows, then up rows
+            tma_load_4d(&tmB, &meta.full[s], sb, k0, t.n_blk * 128, 0, t.e);
+            tma_load_4d(&tmB, &meta.full[s], sb + BNH * BK, k0, t.n_blk * 128, 1, t.e);
+          } else {
+            tma_load_3d(&tmB, &meta.full[s], sb, k0, t.n_blk * BNB, t.e);
           }
           issued++;
           if (++s == stages) {
@@ -503,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nkb = (p.K + BK - 1) / BK, nbn = (p.N + 127) / 128, units = uniform(tiles[p.E] * p.splits);
     const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
     const int r_in_tile = q * 32 + lane;
-    // The current block's quarters: columns half * 32 .. + 31 of the 64 of each weight block,
-    // and their barriers; quarters 0, 1 and 2, 3 take turns by one address bit.
-    uint32_t tq = meta.tmem_slot + ((uint32_t)(q * 32) << 16) + half * 32;
+    // The current block's quarters (one per weight block: columns half * 64 .. + 63 of it) and
+    // their barriers; quarters 0, 1 and 2, 3 take turns by one address bit.
+    uint32_t tq = meta.tmem_slot + ((uint32_t)(q * 32) << 16) + half * 64;
     uint32_t fq = smem_u32(meta.tfull), eq = smem_u32(meta.tempty);
     const uint32_t sfull = smem_u32(meta.sfull), sempty = smem_u32(meta.sempty);
     const uint32_t srow = smem_u32(meta.scale) + r_in_tile * 8;
@@ -534,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = m + r_in_tile < t.rows;
       const int64_t grow = (int64_t)t.row0 + m + r_in_tile;
       const bool live = m + q * 32 < uniform(t.rows);  // whole warp: some row of this quadrant exists
-      // Sums by weight block: acc[b][32 h + i] is row 64 h + 32 half + i of block b.
+      // Sums by weight block: acc[b][i] is row 64 half + i of block b.
       float acc[2][64];
 #pragma unroll
       for (int i = 0; i < 64; i++) acc[0][i] = acc[1][i] = 0.f;
@@ -570,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t nt = h == 0 ? tq + BNH : tq ^ (2 * BNH);
             bool ready = true;
 #pragma unroll
-            for (int c = 0; c < 4; c++) {  // weight block c / 2, columns 16 (c % 2) ..
+            for (int c = 0; c < 4; c++) {  // columns 16 c .. of weight block h
               tmem_ld_wait16(v[c & 1]);
               if (c < 3) {
-                tmem_ld16(tq + h * BNH + ((c + 1) >> 1) * 64 + ((c + 1) & 1) * 16, v[(c + 1) & 1]);
+                tmem_ld16(tq + h * BNH + (c + 1) * 16, v[(c + 1) & 1]);
                 if (c == 1 && asked) ready = test_wait(nf, npar);
               } else {
                 tc_fence_before();
@@ -584,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
 #pragma unroll
               for (int i = 0; i < 16; i++) {
-                float& a = acc[c >> 1][h * 32 + (c & 1) * 16 + i];
-                a = fmaf(__uint_as_float(v[c & 1][i]), f[c >> 1], a);
+                float& a = acc[h][c * 16 + i];
+                a = fmaf(__uint_as_float(v[c & 1][i]), f[h], a);
               }
             }
           }
@@ -599,15 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // instructions, 6 to 17 thousand cycles for a tile, most of them waiting for code.
 #pragma unroll
         for (int i = 0; i < 8; i++)
-          tmem_st16((tq ^ (2 * BNH)) + (i >> 1 & 1) * BNH + (i >> 2) * 64 + (i & 1) * 16, &acc[i >> 2][(i & 3) * 16]);
+          tmem_st16((tq ^ (2 * BNH)) + (i >> 2) * BNH + (i & 3) * 16, &acc[i >> 2][(i & 3) * 16]);
         tmem_st_wait();
       }
 
       // Run c of 16 columns, c < 4: weight block 0, c < 8: block 1; its place in tensor memory
       // and its first row within the block.
       const uint32_t tl = tq ^ (2 * BNH), el = eq ^ 16;
-      auto place = [&](int c) { return tl + (c >> 1 & 1) * BNH + (c >> 2) * 64 + (c & 1) * 16; };
-      auto first_row = [&](int c) { return (c >> 1 & 1) * 64 + half * 32 + (c & 1) * 16; };
+      auto place = [&](int c) { return tl + (c >> 2) * BNH + (c & 3) * 16; };
+      auto first_row = [&](int c) { return half * 64 + (c & 3) * 16; };
       auto fetch = [&](int c, float (&v)[16]) {
         uint32_t r[16];
         tmem_ld16(place(c), r);
@@ -747,7 +744,7 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
   // no group has more than R rows: small batches load a shorter row tile and leave room
   // for more weight stages (the accumulator rows past it are never stored)
   const uint32_t abox = p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
-  constexpr uint32_t brows = 64;  // weight rows per box
+  constexpr uint32_t brows = MODE == FP8_GATED ? BNH : BNB;  // weight rows per box
   CUtensorMap a, b, g;
   const uint64_t dims[2] = {(uint64_t)p.K, (uint64_t)p.R};
   const uint64_t strides[1] = {(uint64_t)p.K};
