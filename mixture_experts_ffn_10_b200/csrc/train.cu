@@ -34,16 +34,19 @@ struct Row {
   uint4 v[L::V > 1 ? L::NV : 1];
   float s[L::V > 1 ? 1 : L::NV];
 
+  // (-inf past E: those values take part in maxima and sums as nothing)
   __device__ __forceinline__ void load(const void* base, int64_t t, int E, int lane) {
     if constexpr (L::V > 1) {
+      constexpr uint32_t inf = L::BF16 ? 0xff80ff80u : 0xff800000u;
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + t * E * (16 / L::V));
 #pragma unroll
       for (int i = 0; i < L::NV; i++)
-        if ((i * L::G + lane) * L::V < E) v[i] = __ldg(p + i * L::G + lane);
+        v[i] = (i * L::G + lane) * L::V < E ? __ldg(p + i * L::G + lane) : make_uint4(inf, inf, inf, inf);
     } else {
 #pragma unroll
       for (int i = 0; i < L::NV; i++) {
         const int e = i * L::G + lane;
+        s[i] = -INFINITY;
         if (e < E)
           s[i] = L::BF16 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(base) + t * E + e))
                          : __ldg(static_cast<const float*>(base) + t * E + e);
@@ -117,10 +120,14 @@ struct Norm {
 
 // l' of the row in l[], scores in s[] (0 past E).  Whole warp.
 template <class L>
-__device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& row, const float (&bias)[L::N], int lane,
+__device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& row, const float (&bias)[L::N],
                                        float (&l)[L::N], float (&s)[L::N]) {
 #pragma unroll
-  for (int n = 0; n < L::N; n++) l[n] = expert_of<L>(n, lane) < a.E ? row.get(n) + bias[n] : -INFINITY;
+  for (int n = 0; n < L::N; n++) l[n] = row.get(n);
+  if (a.router_bias) {
+#pragma unroll
+    for (int n = 0; n < L::N; n++) l[n] += bias[n];
+  }
   Norm z{0.f, 0.f};
   float sum = 0.f;
   if (a.score == MOE_SCORE_SOFTMAX) {
@@ -167,7 +174,7 @@ __device__ __forceinline__ int seq_of(const RouterTrainArgs& a, int t) {
 }
 
 // ---------------------------------------------------------------- balance loss
-constexpr int partial_threads(int n) { return n >= 32 ? 256 : 512; }  // n values of a row per lane
+constexpr int partial_threads(int n) { return n >= 16 ? 256 : 512; }  // n values of a row per lane
 constexpr int kPartialSums = 8192;  // floats of a block's sums: a row of E per warp
 
 template <class L>
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(partial_threads(L::N)) balance_partial_kernel(
       const Row<L> row = next;
       if (t + groups < s1) next.load(a.logits, t + groups, a.E, lane);
       float l[N], s[N];
-      const Norm z = scores<L>(a, row, bias, lane, l, s);
+      const Norm z = scores<L>(a, row, bias, l, s);
       const float f = a.score == MOE_SCORE_SOFTMAX ? 1.f : z.inv_z;
       if (t < s1) {
 #pragma unroll
@@ -314,9 +321,10 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(RouterTrainArgs a)
 
 // ---------------------------------------------------------------- backward
 constexpr int kBackThreads = 256;
+constexpr int back_blocks(int n) { return n <= 8 ? 4 : n <= 16 ? 2 : 1; }  // per SM, n values of a row per lane
 
 template <class L>
-__global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backward_kernel(RouterTrainArgs a) {
+__global__ void __launch_bounds__(kBackThreads, back_blocks(L::N)) router_backward_kernel(RouterTrainArgs a) {
   constexpr int G = L::G, N = L::N, V = L::V;
   constexpr int kSlots = N < 32 / G ? N : 32 / G;  // slots per lane: k <= E, k <= 32
   constexpr int groups = kBackThreads / G;
@@ -365,10 +373,12 @@ __global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backwa
       const int j = q * G + lane;
       s.e[q] = -1;
       s.dw[q] = 0.f;
+      if (q > 0 && q * G >= a.k) continue;  // (uniform: no lane has such a slot)
       if (t < c1 && j < a.k) {
-        const int e = __ldg(a.idx + t * a.k + j);
-        s.e[q] = e >= 0 && e < a.E ? e : -1;
-        s.dw[q] = __ldg(a.dw + t * a.k + j);
+        const int64_t at = t * a.k + j;
+        const int e = __ldg(a.idx + at);
+        s.e[q] = (unsigned)e < (unsigned)a.E ? e : -1;
+        s.dw[q] = __ldg(a.dw + at);
       }
     }
   };
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backwa
     if (t + groups < c1) next.load(a.logits, t + groups, a.E, lane);
     load_slots(t + groups, next_slots);
     float l[N], s[N];
-    const Norm z = scores<L>(a, row, bias, lane, l, s);
+    const Norm z = scores<L>(a, row, bias, l, s);
 
     // balance: A (c_e - sum c p), A = 0 for tokens outside every sequence
     float mean = 0.f;
@@ -422,6 +432,7 @@ __global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backwa
       for (int q = 0; q < kSlots; q++) {
         ss[q] = 0.f;
         sr[q] = 1.f;
+        if (q > 0 && q * G >= a.k) continue;
         if (slots.e[q] >= 0) {
           ss[q] = mine[slots.e[q]];
           if (!soft) sigmoid_pair(ss[q], &ss[q], &sr[q]);
@@ -455,18 +466,21 @@ __global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backwa
 
     // the dense part to the row in shared memory, the slots added there
     float d[N];
+    if (soft) {
+      const float less = fmaf(amp, mean, drop);
 #pragma unroll
-    for (int n = 0; n < N; n++) {
-      const float g = amp * (cnt[n] - mean);
-      if (soft) {
-        d[n] = s[n] * (g - drop);
-      } else {
-        float r = 0.f;
-        if (a.counts) {
-          float se;
+      for (int n = 0; n < N; n++) d[n] = s[n] * fmaf(amp, cnt[n], -less);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; n++) d[n] = 0.f;
+      if (a.counts && amp != 0.f) {
+        const float g = amp * z.inv_z;
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+          float se, r;
           sigmoid_pair(l[n], &se, &r);
+          d[n] = g * (cnt[n] - mean) * se * r;
         }
-        d[n] = amp != 0.f ? g * z.inv_z * s[n] * r : 0.f;
       }
     }
     if (a.dw) {
@@ -528,8 +542,14 @@ __global__ void __launch_bounds__(kBackThreads, L::N <= 8 ? 4 : 1) router_backwa
 }
 
 // ---------------------------------------------------------------- dispatch
+// Vectors of a row per lane, of rows of w vectors of v values.  Fewer lanes per token share
+// the shuffles and the slots among fewer, and more values per lane cost registers and so
+// warps in flight.
+// Loss: two.  65536 x 64 / 65536 x 128 / 32768 x 256 bf16, one, two, four per lane:
+// 18.4 / 21.2 / 22.5, 16.6 / 18.6 / 18.5, 22.8 / 22.6 / 23.1 us.
 template <class L>
 struct Partial {
+  static constexpr int vectors(int w, int) { return w > 1 ? 2 : 1; }
   static cudaError_t go(const RouterTrainArgs& a, cudaStream_t st) {
     int threads = partial_threads(L::N);
     while (threads > 32 && threads / 32 * a.E > kPartialSums) threads /= 2;
@@ -539,37 +559,33 @@ struct Partial {
     return launch_pdl(balance_partial_kernel<L>, (unsigned)a.nchunks, threads, smem, st, a);
   }
 };
+// Backward: eight lanes per token, from 128 experts on 16 values per lane.  The same sizes, 8
+// and 16 values per lane: 18.6 / 24.7 / 22.6, 18.5 / 22.3 / 20.6 us; 65536 x 32 fp32, 4 and 8:
+// 16.4, 20.6 us.
 template <class L>
 struct Backward {
+  static constexpr int vectors(int w, int v) { return w <= 8 ? 1 : w / 8 < 16 / v ? w / 8 : 16 / v; }
   static cudaError_t go(const RouterTrainArgs& a, int sms, cudaStream_t st) {
-    // neighbouring tokens to a block, whole steps of its groups, four blocks per SM at most
+    // neighbouring tokens to a block, whole steps of its groups, one wave
     constexpr int groups = kBackThreads / L::G;
     RouterTrainArgs b = a;
-    const int64_t per = ((int64_t)a.T + (int64_t)sms * 4 - 1) / ((int64_t)sms * 4);
+    const int64_t blocks = (int64_t)sms * back_blocks(L::N), per = (a.T + blocks - 1) / blocks;
     b.chunk = (int)((per + groups - 1) / groups * groups);
     return launch_pdl(router_backward_kernel<L>, (unsigned)((a.T + b.chunk - 1) / b.chunk), kBackThreads,
                       (size_t)kBackThreads * L::N * 4, st, b);
   }
 };
 
-// One vector per lane on the fewest lanes (a power of two) that hold the row, several on 32.
-template <template <class> class Run, int BF16, typename... Args>
+// Rows of up to W vectors (a power of two), Run's share of them per lane and what 32 lanes
+// cannot share otherwise.
+template <template <class> class Run, int BF16, int W, typename... Args>
 cudaError_t by_vectors(const RouterTrainArgs& a, Args... rest) {
   constexpr int V = BF16 ? 8 : 4;
-  const int vectors = a.E / V;
-  if (vectors <= 1) return Run<Layout<BF16, V, 1, 1>>::go(a, rest...);
-  if (vectors <= 2) return Run<Layout<BF16, V, 1, 2>>::go(a, rest...);
-  if (vectors <= 4) return Run<Layout<BF16, V, 1, 4>>::go(a, rest...);
-  if (vectors <= 8) return Run<Layout<BF16, V, 1, 8>>::go(a, rest...);
-  if (vectors <= 16) return Run<Layout<BF16, V, 1, 16>>::go(a, rest...);
-  if (vectors <= 32) return Run<Layout<BF16, V, 1, 32>>::go(a, rest...);
-  if (vectors <= 64) return Run<Layout<BF16, V, 2, 32>>::go(a, rest...);
-  if constexpr (BF16) {
-    return Run<Layout<BF16, V, 4, 32>>::go(a, rest...);
-  } else {
-    if (vectors <= 128) return Run<Layout<BF16, V, 4, 32>>::go(a, rest...);
-    return Run<Layout<BF16, V, 8, 32>>::go(a, rest...);
+  if constexpr (W < kMaxE / V) {
+    if (a.E > W * V) return by_vectors<Run, BF16, 2 * W>(a, rest...);
   }
+  constexpr int share = Run<Layout<BF16, V, 1, 1>>::vectors(W, V), NV = share > W / 32 ? share : W / 32;
+  return Run<Layout<BF16, V, NV, W / NV>>::go(a, rest...);
 }
 template <template <class> class Run, int BF16, typename... Args>
 cudaError_t by_values(const RouterTrainArgs& a, Args... rest) {
@@ -580,7 +596,7 @@ cudaError_t by_values(const RouterTrainArgs& a, Args... rest) {
 }
 template <template <class> class Run, typename... Args>
 cudaError_t by_row(const RouterTrainArgs& a, Args... rest) {
-  if (a.vec) return a.bf16 ? by_vectors<Run, 1>(a, rest...) : by_vectors<Run, 0>(a, rest...);
+  if (a.vec) return a.bf16 ? by_vectors<Run, 1, 1>(a, rest...) : by_vectors<Run, 0, 1>(a, rest...);
   return a.bf16 ? by_values<Run, 1>(a, rest...) : by_values<Run, 0>(a, rest...);
 }
 
