@@ -100,7 +100,9 @@ def balance_loss(cfg, logits, idx, coef=1.0, seq_offsets=None, router_bias=None,
             if nbytes is None:
                 if len(_sizes) > 256:
                     _sizes.clear()
-                nbytes = _sizes[key] = lib.moe_balance_workspace_size(shape, opts, B)
+                nbytes = lib.moe_balance_workspace_size(shape, opts, B)
+                if nbytes:  # (0: the configuration is invalid, as the call below says)
+                    _sizes[key] = nbytes
             workspace = _m.Workspace(nbytes, dev)
         _m._check(lib.moe_balance_loss(shape, opts, logits.data_ptr(), _ptr(router_bias), idx.data_ptr(), _ptr(seq_offsets), B,
                                        coef, counts.data_ptr(), loss.data_ptr(), workspace.ptr, workspace.nbytes,
@@ -156,14 +158,36 @@ class _Route(torch.autograd.Function):
         return (d,) + (None,) * 5
 
 
+_STREAM = "moe_route_stream"
+
+
+def _check_capture(logits):
+    """A leaf's gradient is added on the stream where its eager graph first met it, as long as that
+    graph lives; a captured backward pass that has to join that stream ends the process, so the
+    capture is refused before it begins.  The returned node is to outlive the forward pass."""
+    accumulate = torch.autograd.graph.get_gradient_edge(logits).node  # made here, or a live graph's
+    here = torch.cuda.current_stream(logits.device).cuda_stream
+    if torch.cuda.is_current_stream_capturing() and accumulate.metadata.get(_STREAM, here) != here:
+        raise RuntimeError("route is being captured while outputs of an eager route of the same leaf logits, made on "
+                           "another stream, are alive: release those first, or make them on the capturing stream")
+    accumulate.metadata.setdefault(_STREAM, here)
+    return accumulate
+
+
 def route(cfg, logits, coef=1.0, seq_offsets=None, router_bias=None, selection_bias=None):
     """The layer's routing with its training outputs: (idx [T, k] int32, w [T, k] fp32, loss [] fp32,
     counts [B, E] int32).  w and loss are differentiable with respect to logits, once; the two
     gradients are formed in one pass over the logits.  The biases are constants here (the
-    gradient with respect to router_bias is the sum of dlogits over the tokens)."""
+    gradient with respect to router_bias is the sum of dlogits over the tokens).
+
+    Forward and backward can be captured into a CUDA graph together.  As with any captured
+    backward pass, eager autograd graphs of the same leaves must be gone by then, or have been
+    made on the capturing stream."""
     for name, b in (("router_bias", router_bias), ("selection_bias", selection_bias)):
         if b is not None and b.requires_grad:
             raise ValueError(f"{name} is a constant of route: pass it detached")
     if logits.dim() != 2 or tuple(logits.shape) != (cfg.T, cfg.E) or logits.dtype != _LOGIT_DTYPES[cfg.logit_dtype]:
         raise ValueError(f"logits must be [{cfg.T}, {cfg.E}] {cfg.logit_dtype}")
+    if logits.is_cuda and logits.requires_grad and logits.is_leaf and torch.is_grad_enabled():
+        accumulate = _check_capture(logits)  # noqa: F841
     return _Route.apply(logits.contiguous(), cfg, coef, seq_offsets, router_bias, selection_bias)

@@ -405,3 +405,129 @@ def test_quantize_offsets_past_32_bits(fp8):
     assert torch.equal(s[-3:], rs)
     _same_q(q[-3:], rq)
     assert (q[-7].float() == 0).all()
+
+
+# ------------------------------------------------------------------------------ further calls
+def test_quantize_gate_up(fp8):
+    """The gate rows and the up rows have blocks of their own, a ragged last one each."""
+    w = (torch.randn((3, 2 * 208, 272), generator=_gen(31), device="cuda") * 0.02).to(torch.bfloat16)
+    q, s = fp8.quantize_gate_up(w)
+    assert q.shape == w.shape and s.shape == (3, 4, 3)
+    for half in (0, 1):
+        qh, sh = fp8.quantize_weights(w[:, 208 * half:208 * (half + 1)].contiguous())
+        assert torch.equal(q[:, 208 * half:208 * (half + 1)].view(torch.uint8), qh.view(torch.uint8))
+        assert torch.equal(s[:, 2 * half:2 * half + 2], sh)
+    with pytest.raises(ValueError):
+        fp8.quantize_gate_up(w[:, :7])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=300, E=6, k=1, renormalize=False, bias=True),                          # rows written in place, weighted
+    dict(T=300, E=6, k=1, renormalize=False, weigh_inputs=True),
+    dict(T=3000, d=512, F=512, E=3, k=1, score="sigmoid"),
+    dict(T=200, E=6, k=1, shared_output=True, bias=True),                          # k = 1 with something to add
+    dict(T=3, d=512, F=256, E=300, k=1, renormalize=False),                        # k = 1, sums split along K
+    dict(T=1500, E=5, k=2, weigh_inputs=True, renormalize=False, gu_layout="unfused", bias=True),
+    dict(T=90, d=144, F=272, E=5, k=4, renormalize=False),                         # rows past one block of the sort's few
+    dict(T=256, E=7, k=2), dict(T=257, E=7, k=2),                                  # 512 rows and more
+    dict(T=1, d=7168, F=2048, E=16, k=8, score="sigmoid", routed_scale=2.5),
+])
+def test_layer_variants(moe, kw):
+    c = layer_config(**kw)
+    i = layer_inputs(c)
+    y, idx, w = _run_layer(moe, c, i)
+    check(y, *layer_ref(c, i, idx.long(), w), str(kw))
+    assert torch.equal(y, _run_layer(moe, c, i)[0])
+
+
+def test_non_finite_tokens_stay_alone(moe):
+    """A NaN and an infinity in two tokens' activations: theirs are the only outputs that change."""
+    c = layer_config(T=70, E=4)
+    i = layer_inputs(c)
+    clean, idx, _ = _run_layer(moe, c, i)
+    i["x"][5, 3], i["x"][40, 200] = float("nan"), float("inf")
+    y, idx2, _ = _run_layer(moe, c, i)
+    assert torch.equal(idx, idx2)
+    assert y[5].isnan().all() and y[40].isnan().all()
+    keep = [t for t in range(70) if t not in (5, 40)]
+    assert torch.equal(y[keep], clean[keep])
+
+
+def test_layers_on_two_streams_at_once(moe):
+    """Two layers of different sizes in flight on two streams, each with its workspace."""
+    runs = []
+    for kw in (dict(T=900, d=512, F=1024, E=6), dict(T=12, d=512, F=1024, E=6, seed=3)):
+        c = layer_config(**kw)
+        i = layer_inputs(c)
+        runs.append((c, i, moe.Workspace(moe.moe_workspace_size(moe.shape_of(c), moe.options_of(c))), torch.cuda.Stream(),
+                     moe.forward(c, i)))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for c, i, ws, st, _ in runs:
+            with torch.cuda.stream(st):
+                outs.append(moe.forward(c, i, workspace=ws))
+    torch.cuda.synchronize()
+    for n, y in enumerate(outs):
+        assert torch.equal(y, runs[n % 2][4])
+
+
+def test_static_scratch_and_stage_events(moe):
+    """The entry points beside moe_forward give its output, k = 1 and split sums among them."""
+    stream = torch.cuda.current_stream()
+    for kw in (dict(T=40), dict(T=300, k=1), dict(T=2, d=512, F=512), dict(T=30, Fs=128)):
+        c = layer_config(**kw)
+        i = layer_inputs(c)
+        ref = moe.forward(c, i)
+        shape, opts = moe.shape_of(c), moe.options_of(c)
+        y = torch.full_like(ref, float("nan"))
+        tensors = moe.tensors_of(i, y)
+        assert moe.moe_forward_noalloc(shape, opts, tensors, stream.cuda_stream) == moe.MOE_OK, moe.moe_last_error()
+        assert moe.moe_noalloc_debug_status(stream.cuda_stream) == moe.MOE_OK
+        assert torch.equal(y, ref)
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(moe.MOE_STAGE_EVENTS)]
+        for ev in events:
+            ev.record(stream)
+        ws = moe.Workspace(moe.moe_workspace_size(shape, opts))
+        y.fill_(float("nan"))
+        assert moe.moe_forward_events(shape, opts, tensors, ws.ptr, ws.nbytes, stream.cuda_stream,
+                                      [ev.cuda_event for ev in events]) == moe.MOE_OK
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+        assert all(events[n].elapsed_time(events[n + 1]) >= 0 for n in range(len(events) - 1))
+
+
+def test_kernel_count_is_what_runs(moe):
+    from torch.profiler import ProfilerActivity, profile
+    for kw in (dict(T=4, d=512, F=512), dict(T=300, k=1), dict(T=300), dict(T=700, E=4), dict(T=40, Fs=128)):
+        c = layer_config(**kw)
+        i = layer_inputs(c)
+        ws = moe.Workspace(moe.moe_workspace_size(moe.shape_of(c), moe.options_of(c)))
+        moe.forward(c, i, workspace=ws)
+        torch.cuda.synchronize()
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            moe.forward(c, i, workspace=ws)
+            torch.cuda.synchronize()
+        ours = [e for e in prof.events() if "moe::" in e.name]
+        assert len(ours) == moe.moe_forward_kernel_count(moe.shape_of(c), moe.options_of(c)), [e.name for e in ours]
+
+
+def test_product_on_two_streams_and_of_views(fp8):
+    """Products in flight on two streams with workspaces of their own; operands that are parts of wider buffers."""
+    cases = [_product_case(200, 3, 264, 1024, [60, 40, 100], 1), _product_case(7, 1, 512, 4096, None, 2)]
+    want = [fp8.matmul(*a) for a in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for a, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(fp8.matmul(*a))
+    torch.cuda.synchronize()
+    for n, y in enumerate(got):
+        assert torch.equal(y, want[n % 2])
+    xq, xs, wq, ws, counts = cases[0]
+    padded = torch.zeros((264, 1024), dtype=torch.uint8, device="cuda").view(FP8)
+    padded[32:232] = xq
+    part = fp8.matmul(padded[32:232], xs, wq, ws, counts)
+    assert torch.equal(part, want[0])

@@ -476,3 +476,95 @@ def test_graph_and_streams(train, moe):
     (eager[1].sum() + eager[2]).backward()
     check_gradient(c, logits, leaf.grad, eager[0], torch.ones_like(dw), eager[3], [0, 90, 190], 0.2, 1.0)
     torch.cuda.synchronize()
+
+
+def test_captured_forward_and_backward(train):
+    """A whole training step of the router in one graph, replayed on new inputs: the same gradients as
+    eagerly, bit for bit."""
+    c = config(150, 32, 4, "bf16", "softmax", True)
+    g = _gen(21)
+    x = torch.randn((c.T, 64), generator=g, device="cuda").to(torch.bfloat16)
+    target = torch.randn((c.T, c.k), generator=g, device="cuda")
+    weight = torch.randn((64, c.E), generator=g, device="cuda").to(torch.bfloat16) * 0.3
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step(w):
+        idx, rw, loss, counts = train.route(c, x @ w, coef=0.1)
+        grad, = torch.autograd.grad(((rw - target) ** 2).sum() + loss, w)
+        return idx, loss.detach(), counts, grad
+
+    leaf = weight.clone().requires_grad_()
+    with torch.cuda.stream(side):
+        step(leaf)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(leaf)
+        for seed in (1, 2):
+            x.copy_(torch.randn(x.shape, generator=_gen(seed), device="cuda"))
+            graph.replay()
+            for a, b in zip(out, step(weight.clone().requires_grad_())):
+                assert torch.equal(a, b)
+    torch.cuda.synchronize()
+
+
+def test_capture_beside_an_eager_graph_of_the_same_leaf_is_refused(train):
+    c = config(20, 16, 2)
+    logits, _, _ = inputs(c, 5)
+    leaf = logits.clone().requires_grad_()
+    eager = train.route(c, leaf)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            with pytest.raises(RuntimeError, match="alive"):
+                train.route(c, leaf)
+            y = logits * 2  # the capture goes on
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, logits * 2)
+    (eager[1].sum() + eager[2]).backward()
+    first = leaf.grad.clone()
+    # the eager graph gone, the same leaf is captured, and its gradient is the eager one
+    leaf.grad = None
+    del eager
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = train.route(c, leaf)
+            d, = torch.autograd.grad(out[1].sum() + out[2], leaf)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(d, first)
+
+
+def test_workspace_after_a_refused_configuration(train):
+    """A refusal leaves nothing behind for a valid configuration of the same sizes."""
+    from mixture_experts_ffn_10_b200 import MoeError
+    logits, idx, _ = inputs(config(11, 24, 2))
+    with pytest.raises(MoeError):
+        train.balance_loss(config(11, 24, 2, routed_scale=1.0, n_group=5, topk_group=2), logits, idx)
+    c = config(11, 24, 2)
+    loss, counts = train.balance_loss(c, logits, idx)
+    want = counts64(c, idx, [0, 11])
+    assert torch.equal(counts.long(), want)
+    ref = loss64(c, scores64(c, logits.double())[1], want, [0, 11], 1.0).item()
+    assert abs(loss.item() - ref) <= (24 + 32 + 11 + 20) * 2.0 ** -23 * ref
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [4, 8, 16, 24, 32, 64, 128, 136, 256, 512])
+def test_every_row_width(train, dtype, E):
+    """Rows of every number of vectors and lanes, more tokens than one step of a block, three sequences."""
+    c = config(1500, E, min(E, 8), dtype, "sigmoid" if E % 3 else "softmax", renorm=True)
+    logits, idx, dw = inputs(c, E)
+    off = [0, 333, 334, 1490]
+    seq = offsets(*off)
+    loss, counts = train.balance_loss(c, logits, idx, coef=2.0, seq_offsets=seq)
+    want = counts64(c, idx, off)
+    assert torch.equal(counts.long(), want)
+    ref = loss64(c, scores64(c, logits.double())[1], want, off, 2.0).item()
+    assert abs(loss.item() - ref) <= (E + 32 + 700 + 20) * 2.0 ** -23 * abs(ref)
+    d = train.router_backward(c, logits, idx, dw=dw, counts=counts, coef=2.0, seq_offsets=seq)
+    check_gradient(c, logits, d, idx, dw, want, off, 2.0, 1.0)
