@@ -71,7 +71,7 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
 // Such points (and the e4m3 values) have at most four fraction bits: their low 19 bits are
 // zero.  Next to one, m, the residual x - m s (exact in sign in one fma: m s has 29 bits)
 // tells on which side of m the quotient is.
-static __device__ __noinline__ float fp8_quotient(float x, float s, float hi) {
+__device__ __forceinline__ float fp8_quotient(float x, float s, float hi) {
   float t = x * hi;
   const uint32_t u = __float_as_uint(t) + 16u;
   if ((u & 0x7ffffu) < 32u) {
@@ -231,6 +231,17 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 inline int fp8_n_tiles(int mode, int64_t N) { return (int)((N + (mode == FP8_GATED ? 127 : 255)) / (mode == FP8_GATED ? 128 : 256)); }
 // Upper bound of the row tiles of R rows in E groups: every group adds at most one partial tile.
 inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return R / kFp8BM + (E < R ? E : R); }
+// Ordinary launch: the FP8 GEMMs, and what reads their results, start when everything before
+// them has ended (no programmatic launch: see gemm_fp8.cu).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_ordered(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 // The split factor of a GEMM (1: none).
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms);
 

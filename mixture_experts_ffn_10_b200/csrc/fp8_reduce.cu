@@ -148,18 +148,18 @@ __global__ void __launch_bounds__(kThreads) combine_splits_kernel(Fp8CombineArgs
 cudaError_t launch_fp8_reduce_h(const Fp8GemmArgs& a, const int32_t* off, cudaStream_t st) {
   const int nb = (a.N + 127) / 128;
   const int64_t blocks = ((int64_t)a.R * nb + kThreads / 32 - 1) / (kThreads / 32);
-  return launch_pdl(reduce_h_kernel, (unsigned)blocks, kThreads, 0, st, a, off, nb);
+  return launch_ordered(reduce_h_kernel, (unsigned)blocks, kThreads, 0, st, a, off, nb);
 }
 
 cudaError_t launch_fp8_reduce_y(const Fp8GemmArgs& a, cudaStream_t st) {
   const int64_t blocks = ((int64_t)a.R * (a.N / 4) + kThreads - 1) / kThreads;
-  return launch_pdl(reduce_y_kernel, (unsigned)blocks, kThreads, 0, st, a);
+  return launch_ordered(reduce_y_kernel, (unsigned)blocks, kThreads, 0, st, a);
 }
 
 cudaError_t launch_fp8_combine(const Fp8CombineArgs& a, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
   const dim3 grid(a.T, (a.d / 4 + kThreads - 1) / kThreads);
-  return launch_pdl(combine_splits_kernel, grid, kThreads, 0, st, a);
+  return launch_ordered(combine_splits_kernel, grid, kThreads, 0, st, a);
 }
 
 }  // namespace moe

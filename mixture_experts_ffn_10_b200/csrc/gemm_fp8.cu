@@ -6,15 +6,14 @@
 // The tensor cores form D_b as an fp32 accumulation over one block of K (four K = 32
 // steps) in tensor memory; the scales differ from block to block and row to row, so each
 // D_b is read back and added to an fp32 accumulator with its scale product.  Rows are the
-// MMA's M: a thread of an epilogue warp owns one row and 64 columns of each of the tile's
-// two weight blocks, so a block of K costs it two scale products and 128 multiply-adds,
-// and the accumulators live in its registers for the whole K loop.  (With the weights as M
-// the row scales would differ from register to register and each multiply-add would need
-// an operand from shared memory.)  Tensor memory is a ring of four quarters of 128 columns;
-// a block of K is two MMA groups of N = 128 (one per weight block), each handed over by
-// itself, so that the adds of one quarter run beside the products of the others:
-// with two halves of 256 columns the chain product - hand-over - adds - hand-over of a
-// buffer was longer than two products.
+// MMA's M: a thread of an epilogue warp owns one row and 64 columns of one weight block, so
+// a block of K costs it one scale product and 64 multiply-adds, and the accumulators live
+// in its registers for the whole K loop.  (With the weights as M the row scales would
+// differ from register to register and each multiply-add would need an operand from shared
+// memory.)  Tensor memory is a ring of four quarters of 128 columns; a block of K is two MMA
+// groups of N = 128 (one per weight block), each handed over by itself, so that the adds of
+// one quarter run beside the products of the others: with two halves of 256 columns the
+// chain product - hand-over - adds - hand-over of a buffer was longer than two products.
 //
 // Work: tiles of 128 rows by 256 weight rows (128 gate and their 128 up rows, or 256 plain
 // rows); persistent CTAs, one per SM; the tile list is made on the device from the groups'
@@ -25,10 +24,18 @@
 //   1, 3  MMA issue, blocks of K in turn; 1: TMEM, too;
 //   2     the products of row and weight scales, a ring of blocks ahead in shared memory
 //         (read by the epilogue itself they cost it a memory latency per block);
-//   4-11  epilogue: TMEM lane quadrant x column half.  Their accumulators do not fit the
-//         168 registers that twelve warps leave each: the first four warps hand theirs
-//         over (setmaxnreg, 4 x 104 + 8 x 200 = 12 x 168).
-// Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.
+//   4-19  epilogue: TMEM lane quadrant x 64 columns.  Sixteen warps of 64 accumulators each
+//         fit 96 registers a thread, and four per scheduler hide the tensor memory reads
+//         (eight of 128 with registers handed over from the first four: 4096 rows 368 us
+//         against 366, 77 rows 119 against 123).
+// Large batches are bound by what a tile loads (48 KB per 128 x 256 x 128 from L2 at 64
+// bytes a clock: 770 clocks, the products 512) and by the power limit (clocks of 1.3 to
+// 1.65 GHz): 8192 rows of 8 experts of 4096 x 14336 1.80 ms, 1.6 PFLOP/s; 4096 rows of 32
+// experts of 7168 x 2048 0.37 ms; 8 rows by their weights, 59 us for 201 MB.
+// Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.  Launched in plain stream order,
+// and so is what reads its results: as programmatic launches, a GEMM's CTAs started on SMs
+// that the GEMM before it left free, and 8 rows of 32 experts in a loop of calls ended in an
+// illegal address after some ten thousand (320 thousand calls without: none).
 #include "fp8.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -44,10 +51,9 @@ constexpr int BNB = 256;          // weight rows per tile
 constexpr int BNH = 128;          // of them per MMA group: one of the tile's two weight blocks
 constexpr int kQuarters = 4;      // accumulators of BNH columns in tensor memory
 constexpr int TMEM_COLS = kQuarters * BNH;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;     // tensor memory lane quadrant x 64 of the 256 columns
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
-constexpr int kControlRegs = 104, kEpiRegs = 200;  // of 168 at launch: 4 x 104 + 8 x 200 = 12 x 168
 constexpr int kMaxStages = 6;
 constexpr int kScaleBatch = 8;    // blocks of K whose scale products are handed over together
 constexpr int kScaleSlots = 2 * kScaleBatch;
@@ -61,7 +67,7 @@ constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BNH >> 3) << 17) | ((uint32_t
 // barriers are aligned so that quarters 0, 1 and 2, 3 differ by one address bit.
 struct alignas(64) Meta {
   float2 scale[kScaleSlots][BM];  // [block of K mod slots][row]: times the two weight blocks' scales
-  float amax[2][2][BM];           // [group of 128 columns][column half][row]
+  float amax[4][BM];              // [quarter of the tile's columns][row]
   uint64_t tfull[kQuarters], tempty[kQuarters];
   uint64_t full[kMaxStages], empty[kMaxStages], sfull[2], sempty[2], drain;
   uint32_t tmem_slot;
@@ -111,8 +117,8 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// The two column halves (warps w and w + 4) of a TMEM lane quadrant meet.
-__device__ __forceinline__ void quadrant_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory"); }
+// The four warps of a tensor memory lane quadrant meet.
+__device__ __forceinline__ void quadrant_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
 
 // The same value in every lane, in a form that the compiler knows to be uniform: loops and
 // branches on it need no reconvergence around the whole-warp tensor memory loads (with
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kQuarters; b++) {
       mbar_init(&meta.tfull[b], 1);
-      mbar_init(&meta.tempty[b], kEpiWarps);
+      mbar_init(&meta.tempty[b], kEpiWarps / 2);  // the warps of that weight block
     }
     for (int s = 0; s < 2; s++) {
       mbar_init(&meta.sfull[s], 1);
@@ -340,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t abort = smem_u32(&meta.abort_flag);
 
   if (warp < kFirstEpiWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 0 && elect_one()) {
       // ---------------------------------------------------------- TMA producer
       const int nkb = (p.K + BK - 1) / BK, total = tiles[p.E] * p.splits;
@@ -377,12 +382,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every load issued has landed before the CTA may exit (the last `stages` of them)
+      // before the CTA may exit: every load issued has landed, and the last commit on every
+      // stage's barrier has arrived
       const uint32_t n = issued < (uint32_t)stages ? issued : (uint32_t)stages;
       for (uint32_t j = issued - n; j < issued; j++) {
-        const uint64_t t0 = global_timer();
-        while (!try_wait(full + 8 * (j % stages), (j / stages) & 1) && global_timer() - t0 < kTimeoutNs) {
+        const uint32_t at = 8 * (j % stages), parity = (j / stages) & 1;
+        uint64_t t0 = global_timer();
+        while (!try_wait(full + at, parity) && global_timer() - t0 < kTimeoutNs) {
         }
+        wait(empty + at, parity, abort, p.status);
       }
     } else if ((warp == 1 || warp == 3) && elect_one()) {
       // ---------------------------------------------------------- MMA issuers
@@ -495,213 +503,180 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ------------------------------------------------------------ epilogue
     const int nkb = (p.K + BK - 1) / BK, nbn = (p.N + 127) / 128, units = uniform(tiles[p.E] * p.splits);
-    const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+    const int q = warp & 3, part = (warp - kFirstEpiWarp) >> 2;
+    const int wb = part >> 1, half = part & 1;  // 64 columns of one of the tile's two weight blocks
     const int r_in_tile = q * 32 + lane;
-    // The current block's quarters (one per weight block: columns half * 64 .. + 63 of it) and
-    // their barriers; quarters 0, 1 and 2, 3 take turns by one address bit.
-    uint32_t tq = meta.tmem_slot + ((uint32_t)(q * 32) << 16) + half * 64;
-    uint32_t fq = smem_u32(meta.tfull), eq = smem_u32(meta.tempty);
+    // The current block's quarter for this weight block and its barriers: quarters wb and
+    // wb + 2 take turns by one address bit.
+    const uint32_t lanes0 = meta.tmem_slot + ((uint32_t)(q * 32) << 16);
+    uint32_t tq = lanes0 + wb * BNH + half * 64;
+    uint32_t fq = smem_u32(meta.tfull) + 8 * wb, eq = smem_u32(meta.tempty) + 8 * wb;
     const uint32_t sfull = smem_u32(meta.sfull), sempty = smem_u32(meta.sempty);
-    const uint32_t srow = smem_u32(meta.scale) + r_in_tile * 8;
-    uint32_t n = 0, sn = 0;  // blocks of K so far, and whose scales were read
-    // this row's two scale products of the next block (each block once, in order)
-    auto next_scales = [&]() -> float2 {
-      float2 f;
-      const uint32_t g = 8 * ((sn / kScaleBatch) & 1);
-      if (sn % kScaleBatch == 0) warp_wait(sfull + g, (sn / kScaleSlots) & 1, abort, p.status);
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(f.x), "=f"(f.y)
-                   : "r"(srow + (sn % kScaleSlots) * (BM * 8))
-                   : "memory");
-      if (++sn % kScaleBatch == 0) {
-        __syncwarp();
-        warp_arrive(sempty + g, lane);
-      }
-      return f;
-    };
-    // A wait that gives up does not leave the loop: both halves of a quadrant meet in
-    // every unit, so they walk the same list to its end (the waits then return at once).
+    const uint32_t srow = smem_u32(meta.scale) + r_in_tile * 8 + wb * 4;
+    uint32_t n = 0;  // blocks of K so far
+    // A wait that gives up does not leave the loop: the warps of a quadrant meet in every
+    // unit, so they walk the same list to its end (the waits then return at once).
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_of(p, row0, tiles, u, nkb);
       const int kb0 = uniform(t.kb0), kb1 = uniform(t.kb1);
       const int m = uniform(t.m0);
       const bool valid = m + r_in_tile < t.rows;
       const int64_t grow = (int64_t)t.row0 + m + r_in_tile;
-      const bool live = m + q * 32 < uniform(t.rows);  // whole warp: some row of this quadrant exists
-      // Sums by weight block: acc[b][i] is row 64 half + i of block b.
-      float acc[2][64];
+      const bool live = m + q * 32 < uniform(t.rows);  // the whole quadrant: some row of it exists
+      float acc[64];
 #pragma unroll
-      for (int i = 0; i < 64; i++) acc[0][i] = acc[1][i] = 0.f;
-      if (!live) {
-        for (int kb = kb0; kb < kb1; kb++, n++) {
-          next_scales();
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            warp_wait(fq + 8 * h, (n >> 1) & 1, abort, p.status);
-            warp_arrive(eq + 8 * h, lane);
-          }
-          tq ^= 2 * BNH;
-          fq ^= 16;
-          eq ^= 16;
+      for (int i = 0; i < 64; i++) acc[i] = 0.f;
+      for (int left = kb1 - kb0; left > 0; left--, n++) {
+        // this row's scale product of the block
+        const uint32_t g = 8 * ((n / kScaleBatch) & 1);
+        if (n % kScaleBatch == 0) warp_wait(sfull + g, (n / kScaleSlots) & 1, abort, p.status);
+        float f;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(srow + (n % kScaleSlots) * (BM * 8)) : "memory");
+        if ((n + 1) % kScaleBatch == 0) {
+          __syncwarp();
+          warp_arrive(sempty + g, lane);
         }
-      } else if (kb0 < kb1) {
-        // One run of 16 columns after another through all quarters: while 16 columns are
-        // added the next 16 are on their way, the next quarter's first ones too, and whether
-        // that quarter is ready is asked before the adds in between (the answer takes some
-        // hundred cycles on a busy SM).
-        uint32_t v[2][16];
-        float2 next = next_scales();
         warp_wait(fq, (n >> 1) & 1, abort, p.status);
-        tc_fence_after();
-        tmem_ld16(tq, v[0]);
-        for (int left = kb1 - kb0; left > 0; left--, n++) {
-          const float f[2] = {next.x, next.y};
-          if (left > 1) next = next_scales();
+        if (live) {
+          tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const bool asked = h == 0 || left > 1;
-            const uint32_t nf = h == 0 ? fq + 8 : fq ^ 16, npar = ((n + h) >> 1) & 1;
-            const uint32_t nt = h == 0 ? tq + BNH : tq ^ (2 * BNH);
-            bool ready = true;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {  // columns 16 c .. of weight block h
-              tmem_ld_wait16(v[c & 1]);
-              if (c < 3) {
-                tmem_ld16(tq + h * BNH + (c + 1) * 16, v[(c + 1) & 1]);
-                if (c == 1 && asked) ready = test_wait(nf, npar);
-              } else {
-                tc_fence_before();
-                if (left > 1) warp_arrive(eq + 8 * h, lane);  // the last block's quarters are kept
-                if (asked && !__all_sync(0xffffffffu, ready)) warp_wait(nf, npar, abort, p.status);
-                tc_fence_after();
-                tmem_ld16(nt, v[0]);  // (after the last quarter: whatever the next holds, not used)
-              }
-#pragma unroll
-              for (int i = 0; i < 16; i++) {
-                float& a = acc[h][c * 16 + i];
-                a = fmaf(__uint_as_float(v[c & 1][i]), f[h], a);
-              }
+          for (int c = 0; c < 4; c++) {
+            uint32_t v[16];
+            tmem_ld16(tq + c * 16, v);
+            tmem_ld_wait16(v);
+            if (c == 3) {
+              tc_fence_before();
+              if (left > 1) warp_arrive(eq, lane);  // the last block's quarter is kept
             }
-          }
-          tq ^= 2 * BNH;
-          fq ^= 16;
-          eq ^= 16;
-        }
-        tmem_ld_wait16(v[0]);
-        // The sums go back to tensor memory, to this thread's columns of the quarters kept, for
-        // the loops below to walk: unrolled over registers, what follows was some 2500
-        // instructions, 6 to 17 thousand cycles for a tile, most of them waiting for code.
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          tmem_st16((tq ^ (2 * BNH)) + (i >> 2) * BNH + (i & 3) * 16, &acc[i >> 2][(i & 3) * 16]);
+            for (int i = 0; i < 16; i++) acc[c * 16 + i] = fmaf(__uint_as_float(v[i]), f, acc[c * 16 + i]);
+          }
+        } else {
+          warp_arrive(eq, lane);
+        }
+        tq ^= 2 * BNH;
+        fq ^= 16;
+        eq ^= 16;
+      }
+      // The sums go back to tensor memory, to this thread's columns of the quarter kept, for
+      // the loops below to walk: unrolled over registers, what follows was some 2500
+      // instructions, 6 to 17 thousand cycles for a tile, most of them waiting for code.
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) tmem_st16((tq ^ (2 * BNH)) + i * 16, &acc[i * 16]);
         tmem_st_wait();
       }
 
-      // Run c of 16 columns, c < 4: weight block 0, c < 8: block 1; its place in tensor memory
-      // and its first row within the block.
-      const uint32_t tl = tq ^ (2 * BNH), el = eq ^ 16;
-      auto place = [&](int c) { return tl + (c >> 2) * BNH + (c & 3) * 16; };
-      auto first_row = [&](int c) { return half * 64 + (c & 3) * 16; };
-      auto fetch = [&](int c, float (&v)[16]) {
+      // Columns of the kept quarters (weight block b's from column 0) in this thread's lane;
+      // this warp's own 64 in runs of 16.
+      const uint32_t kept = (tq ^ (2 * BNH)) - (wb * BNH + half * 64), el = eq ^ 16;
+      auto fetch = [&](uint32_t at, float (&v)[16]) {
         uint32_t r[16];
-        tmem_ld16(place(c), r);
+        tmem_ld16(at, r);
         tmem_ld_wait16(r);
 #pragma unroll
         for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
       };
-      auto give_back = [&]() {
-        tc_fence_before();
-        warp_arrive(el, lane);
-        warp_arrive(el + 8, lane);
-      };
+      const int c0 = wb * BNH + half * 64;  // the warp's first column of the tile's 256
       if (p.splits > 1) {
         if (live) {
-          float* out = p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB;
+          float* out = p.partial + ((int64_t)t.sp * p.R + grow) * p.pitch + t.n_blk * BNB + c0;
 #pragma unroll 1
-          for (int c = 0; c < 8; c++) {
+          for (int c = 0; c < 4; c++) {
             float v[16];
-            fetch(c, v);
+            fetch(kept + c0 + c * 16, v);
             if (valid) {
-              float4* o = reinterpret_cast<float4*>(out + (c >> 2) * 128 + first_row(c));
+              float4* o = reinterpret_cast<float4*>(out + c * 16);
 #pragma unroll
               for (int i = 0; i < 4; i++) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
-          give_back();
+          tc_fence_before();
+          warp_arrive(el, lane);
         }
         continue;
       }
       if (MODE == FP8_LINEAR) {
         if (live) {
           const float w = p.roww && valid ? p.roww[grow] : 1.f;
-          const int64_t orow = p.y_row && valid ? p.y_row[grow] : grow;
+          int64_t orow = grow;
+          bool stored = valid;
+          if (p.y_row && valid) {
+            orow = p.y_row[grow];
+            if (orow < 0 || orow >= p.R) {
+              set_status(p.status, MOE_ERR_SHAPE);
+              stored = false;
+            }
+          }
           const uint16_t* bias = p.bias ? p.bias + (int64_t)t.e * p.N : nullptr;
 #pragma unroll 1
-          for (int c = 0; c < 8; c++) {
+          for (int c = 0; c < 4; c++) {
             float v[16];
-            fetch(c, v);
-            const int n0 = t.n_blk * BNB + (c >> 2) * 128 + first_row(c);
+            fetch(kept + c0 + c * 16, v);
+            const int n0 = t.n_blk * BNB + c0 + c * 16;
             if (bias) add_bias(v, bias, n0, p.N);
             uint16_t* out = p.y + orow * p.N + n0;
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
-              if (valid && n0 + i < p.N)  // N is a multiple of 8
+              if (stored && n0 + i < p.N)  // N is a multiple of 8
                 *reinterpret_cast<uint4*>(out + i) =
                     make_uint4(pack_bf16x2(v[i] * w, v[i + 1] * w), pack_bf16x2(v[i + 2] * w, v[i + 3] * w),
                                pack_bf16x2(v[i + 4] * w, v[i + 5] * w), pack_bf16x2(v[i + 6] * w, v[i + 7] * w));
             }
           }
-          give_back();
+          tc_fence_before();
+          warp_arrive(el, lane);
         }
         continue;
       }
       // gated / plain: activate (back into tensor memory), agree on each row's largest
-      // magnitude per 128 features, round.  Gated: one group per tile (block 0 gate, block 1
-      // up); plain: two.
-      constexpr int kRuns = MODE == FP8_GATED ? 4 : 8;  // of 16 features
+      // magnitude per 128 features, round.  Gated: block 0 holds the gate sums and block 1
+      // the up sums of 128 features, 32 of them for each of the quadrant's four warps;
+      // plain: 128 features per block, 64 for each of its two.
+      constexpr bool kGated = MODE == FP8_GATED;
+      constexpr int kRuns = kGated ? 2 : 4;  // of 16 features
+      const int col = kGated ? part * 32 : c0;
+      const int grp = kGated ? t.n_blk : 2 * t.n_blk + wb;
+      const int f_first = kGated ? t.n_blk * 128 + col : t.n_blk * BNB + col;
       if (live) {
+        tc_fence_before();
+        quadrant_sync(q);  // the quadrant's sums are in tensor memory
+        tc_fence_after();
         const Fp8Bias bias = fp8_bias(MODE, p.layout, t.e, p.N, p.bias, p.gate_bias);
         float m = 0.f;
 #pragma unroll 1
         for (int c = 0; c < kRuns; c++) {
           float g[16], u[16];
-          fetch(c, g);
-          if (MODE == FP8_GATED) fetch(c + 4, u);
-          const int f0 = (MODE == FP8_GATED ? t.n_blk * 128 : t.n_blk * BNB + (c >> 2) * 128) + first_row(c);
+          fetch(kept + col + c * 16, g);
+          if (kGated) fetch(kept + BNH + col + c * 16, u);
+          const int f0 = f_first + c * 16;
           if (bias.g) add_bias(g, bias.g, f0, p.N);
           if (bias.u) add_bias(u, bias.u, f0, p.N);
-          m = fmaxf(m, activate<MODE == FP8_GATED>(g, u, p.act, f0, p.N));
-          tmem_st16(place(c), g);
-          if ((c & 3) == 3) {
-            meta.amax[c >> 2][half][r_in_tile] = m;
-            m = 0.f;
-          }
+          m = fmaxf(m, activate<kGated>(g, u, p.act, f0, p.N));
+          tmem_st16(kept + col + c * 16, g);
         }
+        meta.amax[part][r_in_tile] = m;
         tmem_st_wait();
-      }
-      quadrant_sync(q);
-      if (live) {
-        Fp8Scale s{};
+        quadrant_sync(q);
+        m = fmaxf(meta.amax[part][r_in_tile], meta.amax[part ^ 1][r_in_tile]);
+        if (kGated) m = fmaxf(m, fmaxf(meta.amax[part ^ 2][r_in_tile], meta.amax[part ^ 3][r_in_tile]));
+        const Fp8Scale s = fp8_scale_of(m);
+        if (valid && (kGated ? part == 0 : half == 0) && grp < nbn) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s.s;
 #pragma unroll 1
         for (int c = 0; c < kRuns; c++) {
-          const int grp = MODE == FP8_GATED ? t.n_blk : 2 * t.n_blk + (c >> 2);
-          if ((c & 3) == 0) {
-            s = fp8_scale_of(fmaxf(meta.amax[c >> 2][0][r_in_tile], meta.amax[c >> 2][1][r_in_tile]));
-            if (valid && half == 0 && grp < nbn) p.hs[grow * p.hs_row + (int64_t)grp * p.hs_grp] = s.s;
-          }
           float h[16];
-          fetch(c, h);
-          const int f0 = grp * 128 + first_row(c);
+          fetch(kept + col + c * 16, h);
+          const int f0 = f_first + c * 16;
           if (valid && f0 < p.N)  // N is a multiple of 16
             *reinterpret_cast<uint4*>(p.hq + grow * p.N + f0) =
                 make_uint4(fp8_round4(h, s), fp8_round4(h + 4, s), fp8_round4(h + 8, s), fp8_round4(h + 12, s));
         }
-        give_back();
+        tc_fence_before();
+        quadrant_sync(q);  // both quarters and the maxima are read before they are written again
+        warp_arrive(el, lane);
       }
-      quadrant_sync(q);  // the maxima are read before the next tile's are written
     }
   }
 
@@ -732,11 +707,13 @@ template <int MODE, int ABOX>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& g, const Fp8GemmArgs& p, cudaStream_t st) {
   const int stages = stages_for(ABOX, p.E);
   const int smem = 1024 + stages * stage_bytes(ABOX) + meta_bytes(p.E);
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the most, whatever E needs: another thread may launch the same kernel for more groups)
+  cudaError_t e =
+      cudaFuncSetAttribute(fp8_gemm_kernel<MODE, ABOX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.max_tiles * p.splits;
   const unsigned grid = (unsigned)(units < p.num_sms ? units : p.num_sms);
-  return launch_pdl(fp8_gemm_kernel<MODE, ABOX>, grid, kThreads, smem, st, a, b, g, p, stages);
+  return launch_ordered(fp8_gemm_kernel<MODE, ABOX>, grid, kThreads, smem, st, a, b, g, p, stages);
 }
 
 template <int MODE>
