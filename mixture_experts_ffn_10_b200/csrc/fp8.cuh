@@ -229,8 +229,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 
 // N tiles of a GEMM: 256 accumulator columns (128 gated features).
 inline int fp8_n_tiles(int mode, int64_t N) { return (int)((N + (mode == FP8_GATED ? 127 : 255)) / (mode == FP8_GATED ? 128 : 256)); }
-// Upper bound of the row tiles of R rows in E groups: every group adds at most one partial tile.
-inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return R / kFp8BM + (E < R ? E : R); }
+// Upper bound of the row tiles of R rows in E groups: r rows fill at most (r + 127) / 128.
+inline int64_t fp8_m_tiles(int64_t R, int64_t E) { return (R + (E < R ? E : R) * (kFp8BM - 1)) / kFp8BM; }
 // Ordinary launch: the FP8 GEMMs, and what reads their results, start when everything before
 // them has ended (no programmatic launch: see gemm_fp8.cu).
 template <typename... KArgs, typename... Args>

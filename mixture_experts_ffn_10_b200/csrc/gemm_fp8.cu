@@ -719,7 +719,8 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
 template <int MODE>
 cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
   // no group has more than R rows: small batches load a shorter row tile and leave room
-  // for more weight stages (the accumulator rows past it are never stored)
+  // for more weight stages (the accumulator rows past it are never stored); 16 experts of
+  // 2880 x 2880, against tiles of 128: 32 rows 117, 123 us, 64 rows 119, 121
   const uint32_t abox = p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
   constexpr uint32_t brows = MODE == FP8_GATED ? BNH : BNB;  // weight rows per box
   CUtensorMap a, b, g;
@@ -749,8 +750,25 @@ cudaError_t launch_mode(const Fp8GemmArgs& p, cudaStream_t st) {
 }  // namespace
 
 int fp8_splits(int mode, int64_t R, int64_t E, int64_t N, int64_t K, int sms) {
-  if (R > kSplitMaxRows) return 1;
-  return choose_splits(fp8_m_tiles(R, E) * fp8_n_tiles(mode, N), (int)((K + BK - 1) / BK), sms);
+  // In blocks of K of one tile (0.47 us): a unit's fixed cost, the reduction's launch, and the
+  // partial sums written and read at 4.2 TB/s.  Split and whole: 1 row of 7168 x 4096 22.5,
+  // 32.8 us; 384 rows 32.8, 41.0; 1 row through experts of 4096 x 2048 41, 47; 512 rows of
+  // 4096 x 4096 (not split by this) 33, 29.
+  constexpr int kUnit = 8, kReduce = 8, kMost = 8;
+  constexpr double kBytes = 2e6;
+  const int64_t tiles = fp8_m_tiles(R, E) * fp8_n_tiles(mode, N), nkb = (K + BK - 1) / BK;
+  if (tiles <= 0 || tiles >= sms) return 1;
+  const double sums = (double)R * fp8_n_tiles(mode, N) * BNB * 8 / kBytes;
+  int best = 1;
+  double best_cost = nkb + kUnit;
+  for (int s = 2; s <= kMost && 2 * s <= nkb; s++) {
+    const double cost = (double)((tiles * s + sms - 1) / sms * ((nkb + s - 1) / s + kUnit) + kReduce) + s * sums;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, cudaStream_t st) {

@@ -51,7 +51,12 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without its object: 2 us less
+
+
 def _stream(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
     return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
 
 
@@ -77,8 +82,8 @@ def quantize(x, stream=None):
     if pitch < K:
         raise ValueError("the rows of x overlap")
     with _on(x.device):
-        q = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((R, _cdiv(K, BLOCK)), dtype=torch.float32, device=x.device)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        s = x.new_empty((R, _cdiv(K, BLOCK)), dtype=torch.float32)
         _m._check(_library().moe_fp8_quantize(_dtype_code(x), R, K, x.data_ptr(), pitch, q.data_ptr(), s.data_ptr(),
                                               _stream(stream, x.device)))
     return q, s

@@ -92,8 +92,8 @@ def balance_loss(cfg, logits, idx, coef=1.0, seq_offsets=None, router_bias=None,
     dev = logits.device
     with _on(dev):
         lib, (shape, opts) = _library(), _config(cfg)
-        counts = torch.empty((B, cfg.E), dtype=torch.int32, device=dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
+        counts = idx.new_empty((B, cfg.E))
+        loss = logits.new_empty((), dtype=torch.float32)
         if workspace is None:
             key = (cfg.T, cfg.E, B)  # what the size depends on
             nbytes = _sizes.get(key)

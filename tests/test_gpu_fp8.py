@@ -531,3 +531,27 @@ def test_product_on_two_streams_and_of_views(fp8):
     padded[32:232] = xq
     part = fp8.matmul(padded[32:232], xs, wq, ws, counts)
     assert torch.equal(part, want[0])
+
+
+def test_calls_in_a_loop(moe):
+    """Twenty thousand calls back to back, each with a workspace and an output of its own from the allocator,
+    tiles for fewer CTAs than the GPU has SMs: every output the first one's."""
+    from mixture_experts_ffn_10_b200.ep import LibraryOps
+    c = layer_config(T=8, d=2048, F=2048, E=32, k=1)
+    i = layer_inputs(c)
+    sets = []
+    for n in range(3):
+        g = _gen(90 + n)
+        e = torch.randperm(32, generator=g, device="cuda")[:8].to(torch.int32)
+        sets.append((torch.randn((8, c.d), generator=g, device="cuda").to(torch.bfloat16), e,
+                     torch.rand(8, generator=g, device="cuda")))
+    ops = LibraryOps()
+    refs = [ops.experts_forward(c, *s, i) for s in sets]
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(20000):
+        y = ops.experts_forward(c, *sets[n % 3], i)
+        if n % 7 == 0:
+            wrong += (y.view(torch.int16) != refs[n % 3].view(torch.int16)).any()
+        if n % 1000 == 0:
+            torch.cuda.synchronize()
+    assert int(wrong) == 0
