@@ -33,7 +33,7 @@
 // 1.65 GHz): 8192 rows of 8 experts of 4096 x 14336 1.80 ms, 1.6 PFLOP/s; 4096 rows of 32
 // experts of 7168 x 2048 0.37 ms; 8 rows by their weights, 59 us for 201 MB.
 // Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.  Launched in plain stream order,
-// and so is what reads its results: as programmatic launches, a GEMM's CTAs started on SMs
+// and nothing starts before its end: as programmatic launches, a GEMM's CTAs started on SMs
 // that the GEMM before it left free, and 8 rows of 32 experts in a loop of calls ended in an
 // illegal address after some ten thousand (320 thousand calls without: none).
 #include "fp8.cuh"
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&meta.tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_enter();
+  // (no pdl_enter(): launched when everything before has ended, and nothing starts before its end)
   if (p.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
   for (int e = threadIdx.x; e < p.E; e += kThreads) row0[e] = p.cnt ? p.cnt[e] : p.R;
   tc_fence_before();
