@@ -555,3 +555,25 @@ def test_calls_in_a_loop(moe):
         if n % 1000 == 0:
             torch.cuda.synchronize()
     assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("rows", [8, 700])
+def test_expert_rows_with_invalid_experts(moe, rows):
+    """An expert index outside the stack is reported in the status word; the other rows are right."""
+    c = layer_config(T=rows, E=32, k=1, d=512, F=512)
+    i = layer_inputs(c)
+    g = _gen(rows)
+    e = torch.randint(0, 32, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    e[1], e[rows - 2] = -1, 32
+    w = torch.rand(rows, generator=g, device="cuda")
+    shape, opts = moe.shape_of(c), moe.options_of(c)
+    ws = moe.Workspace(moe.moe_workspace_size(shape, opts))
+    ws.buf.fill_(0xA5)
+    y = torch.empty_like(i["x"])
+    tensors = moe.tensors_of({k: v for k, v in i.items() if k != "logits"}, y)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert moe.moe_experts_forward(shape, opts, tensors, e.data_ptr(), w.data_ptr(), ws.ptr, ws.nbytes, stream) == moe.MOE_OK
+    assert moe.STATUS_NAMES[moe.moe_debug_status(ws.ptr, stream)] == "MOE_ERR_SHAPE"
+    keep = [r for r in range(rows) if r not in (1, rows - 2)]
+    ref, tol = layer_ref(c, i, e.clamp(0, 31).long()[:, None], w[:, None])
+    check(y[keep], ref[keep], tol[keep])
