@@ -41,14 +41,16 @@ extern "C" {
  * must divide E (0: global indices).  The workspace is moe_workspace_size(shape, opts)
  * bytes, as for moe_forward.  Errors: MOE_ERR_NULL / ARG / ALIGN / WORKSPACE before
  * any launch; an expert index outside [0, E) in idx is MOE_ERR_SHAPE in the workspace
- * status word (moe_debug_status). */
+ * status word (moe_debug_status), its slot has no row (pos -1), and the rows past the
+ * others are not written. */
 MOE_API int moe_permute(const moe_shape *shape, const moe_options *opts, const int32_t *idx, const float *w,
                         const void *x, void *x_perm, int32_t *row_expert, float *row_w, int32_t *expert_counts,
                         int32_t *pos, int experts_per_rank, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The expert FFNs of rows that arrive with their expert: shape.T rows x [T, d] (in
  * tensors->x), shape.E the experts held here (the stacks in tensors), shape.k = 1,
- * row_expert [T] int32 in [0, E), row_w [T] fp32.  y[r] = row_w[r] * FFN_e(x[r]) as
+ * row_expert [T] int32 in [0, E) (one outside is MOE_ERR_SHAPE in the status word and
+ * leaves the other rows as they are without it), row_w [T] fp32.  y[r] = row_w[r] * FFN_e(x[r]) as
  * moe_forward's expert outputs (with weigh_inputs: FFN_e(row_w[r] * x[r])), in
  * tensors->y.  Routing options are not used; router_logits, router_weight, topk_idx,
  * topk_w and logits_out must be NULL; no shared expert (Fs = 0).  Otherwise as

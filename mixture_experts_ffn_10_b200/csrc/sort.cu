@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
       my_w = a.roww[my_row];
     }
   }
-  if (__any_sync(0xffffffffu, my_row < 0)) return;
   // four vectors per lane in flight: loads first, then the k (scaled) stores of each;
   // every lane runs every iteration (the shuffles below need the whole warp)
   constexpr int kBatch = 4;
@@ -149,6 +148,7 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
     for (int j = 0; j < a.k; j++) {
       const int row = __shfl_sync(0xffffffffu, my_row, j);
       const float w = __shfl_sync(0xffffffffu, my_w, j);
+      if (row < 0) continue;  // a slot without an expert has no row
       uint4* dst = reinterpret_cast<uint4*>((T*)a.xg + (int64_t)row * a.d);
 #pragma unroll
       for (int b = 0; b < kBatch; b++) {

@@ -123,7 +123,8 @@ __device__ void segment_scan(const SortArgs& a, int32_t* cnt, int32_t* tg, int32
 
 // Stable in-order placement of the (t, j) entries n0 .. n0 + n_ent - 1 of one chunk by
 // one warp: row = first row of the expert + `before` (rows of earlier chunks, or null)
-// + run (earlier entries of this chunk; run[] zeroed, in shared memory).
+// + run (earlier entries of this chunk; run[] zeroed, in shared memory).  An entry without
+// an expert gets the position -1: what the workspace held there may be another entry's row.
 __device__ inline void scatter_chunk(const SortArgs& a, int t0, int n_ent, const int32_t* first_row,
                               const int32_t* before, int32_t* run) {
   const int lane = threadIdx.x & 31;
@@ -144,8 +145,11 @@ __device__ inline void scatter_chunk(const SortArgs& a, int t0, int n_ent, const
         a.perm[row] = t;
         a.roww[row] = a.w[slot];
       } else {
+        a.pos[slot] = -1;
         set_status(a.status, MOE_ERR_SHAPE);
       }
+    } else if (valid) {
+      a.pos[slot] = -1;
     }
     __syncwarp();
     if (e >= 0 && rank == 0) run[e] += __popc(peers);
