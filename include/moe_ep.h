@@ -49,8 +49,8 @@ MOE_API int moe_permute(const moe_shape *shape, const moe_options *opts, const i
 
 /* The expert FFNs of rows that arrive with their expert: shape.T rows x [T, d] (in
  * tensors->x), shape.E the experts held here (the stacks in tensors), shape.k = 1,
- * row_expert [T] int32 in [0, E) (one outside is MOE_ERR_SHAPE in the status word and
- * leaves the other rows as they are without it), row_w [T] fp32.  y[r] = row_w[r] * FFN_e(x[r]) as
+ * row_expert [T] int32 in [0, E) (one outside is MOE_ERR_SHAPE in the status word; its
+ * row of y is 0 and the other rows are as without it), row_w [T] fp32.  y[r] = row_w[r] * FFN_e(x[r]) as
  * moe_forward's expert outputs (with weigh_inputs: FFN_e(row_w[r] * x[r])), in
  * tensors->y.  Routing options are not used; router_logits, router_weight, topk_idx,
  * topk_w and logits_out must be NULL; no shared expert (Fs = 0).  Otherwise as

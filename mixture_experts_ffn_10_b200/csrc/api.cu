@@ -348,9 +348,12 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
   const bool fp8 = s->w_dtype == MOE_FP8;
   const Fp8Regions fr = fp8 ? fp8_regions(p.R, p.d, p.F, p.E) : Fp8Regions{};
   const size_t fp8_base = p.total - fr.total;  // the FP8 operands end the workspace
+  // FP8, one expert per token and nothing to add: the expert's row is the token's output
+  const bool direct = fp8 && p.k == 1 && p.Fs == 0 && !t->shared_output && p.splits_dn == 1;
   if (fp8) {
     const Fp8GatherArgs ga{static_cast<const uint16_t*>(t->x), sa.pos, sa.roww, at<uint8_t>(ws, fp8_base + fr.xq),
-                           at<float>(ws, fp8_base + fr.xs), (int)p.R, (int)p.d, (int)p.T, (int)p.k, o->weigh_inputs, status};
+                           at<float>(ws, fp8_base + fr.xs), (int)p.R, (int)p.d, (int)p.T, (int)p.k, o->weigh_inputs, status,
+                           direct ? static_cast<uint16_t*>(t->y) : nullptr};
     if ((e = launch_fp8_gather(ga, st)) != cudaSuccess) return cuda_fail(e, "gather kernel");
   } else if (!p.direct_x) {
     GatherArgs ga{t->x, sa.pos, sa.roww, at<void>(ws, p.o_x), (int)p.R, (int)p.d, (int)p.T, (int)p.k,
@@ -470,8 +473,6 @@ int run(const moe_shape* s, const moe_options* o, const moe_tensors* t, void* ws
     fd.gate_bias = nullptr;
     fd.roww = o->weigh_inputs ? nullptr : sa.roww;
     fd.y = at<uint16_t>(ws, p.o_y);
-    // one expert per token and nothing to add: the expert's row is the token's output
-    const bool direct = p.k == 1 && p.Fs == 0 && !t->shared_output && p.splits_dn == 1;
     if (direct) {
       fd.y = static_cast<uint16_t*>(t->y);
       fd.y_row = sa.perm;

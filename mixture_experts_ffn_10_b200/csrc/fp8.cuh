@@ -183,6 +183,7 @@ struct Fp8GatherArgs {
   float* xs;            // [ceil(d / 128), R]
   int R, d, T, k, weigh_inputs;
   int* status;
+  uint16_t* y;          // k = 1 with rows written in place: [T, d], zeros for a token without an expert; or null
 };
 cudaError_t launch_fp8_gather(const Fp8GatherArgs& a, cudaStream_t st);
 

@@ -275,6 +275,11 @@ __global__ void __launch_bounds__(kThreads) gather_quantize_kernel(Fp8GatherArgs
       const int row = a.pos[(int64_t)tok[i] * a.k + j];
       if (row < 0 || row >= a.R) {
         set_status(a.status, MOE_ERR_SHAPE);
+        // no row of the down product is this token's: its output is the empty sum, as a combine's
+        if (a.y && col < a.d) {
+          uint4* out = reinterpret_cast<uint4*>(a.y + (int64_t)tok[i] * a.d + col);
+          out[0] = out[1] = make_uint4(0, 0, 0, 0);
+        }
         continue;
       }
       if (a.weigh_inputs) {

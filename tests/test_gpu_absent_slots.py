@@ -99,3 +99,21 @@ def test_permute_of_absent_slots(moe, T, dtype):
     assert torch.equal(at.sort().values, torch.arange(int(ok.sum()), device="cuda"))
     tok = torch.arange(T, device="cuda")[:, None].expand(T, k)[ok]
     assert torch.equal(rows[at], x[tok]) and torch.equal(row_expert[at], bad[ok]) and torch.equal(row_w[at], w[ok])
+
+
+@pytest.mark.parametrize("w_dtype", ["fp8", "bf16"])
+@pytest.mark.parametrize("rows,kw", [(10, {}), (10, dict(d=2048, F=2048, E=32)), (700, {}), (1200, dict(weigh_inputs=True)),
+                                     (333, dict(d=144, F=272))])
+def test_output_rows_of_absent_experts_are_zero(moe, w_dtype, rows, kw):
+    """The empty sum, whether the rows go through a combine (sums split along K, bf16) or are written in place."""
+    c = layer_config(**{**dict(T=rows, E=6, k=1, d=512, F=512, w_dtype=w_dtype), **kw})
+    i = layer_inputs(c)
+    if w_dtype == "bf16":
+        i = _bf16_inputs(c, i)
+    e, bad, gone, w = _absent(rows, c.E)
+    ws = moe.Workspace(moe.moe_workspace_size(moe.shape_of(c), moe.options_of(c)))
+    y = torch.full_like(i["x"], float("nan"))
+    assert _experts(moe, c, i, bad, w, ws, y) == "MOE_ERR_SHAPE"
+    assert (y[gone] == 0).all() and y.isfinite().all()
+    assert _experts(moe, c, i, torch.full_like(bad, -1), w, ws, y.fill_(float("nan"))) == "MOE_ERR_SHAPE"
+    assert (y == 0).all()
