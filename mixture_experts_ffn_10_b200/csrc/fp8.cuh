@@ -128,7 +128,11 @@ __device__ __forceinline__ void fp8_round16_bf16(const float (&x)[16], const Fp8
   for (int i = 0; i < 16; i++) t[i] = x[i] * f.inv;
   if (__any_sync(0xffffffffu, f.fix != 0.f)) {
 #pragma unroll
-    for (int i = 0; i < 16; i++) t[i] = fmaf(-fmaf(t[i], f.s, -x[i]), f.fix, t[i]);  // (keeps -0)
+    for (int i = 0; i < 16; i++) {
+      // (keeps -0; a lane without a correction keeps its quotients: 0 times an infinite scale is no 0)
+      const float c = fmaf(-fmaf(t[i], f.s, -x[i]), f.fix, t[i]);
+      if (f.fix != 0.f) t[i] = c;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; i++) w[i] = fp8_pack4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
