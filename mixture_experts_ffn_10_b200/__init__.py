@@ -13,6 +13,7 @@ helpers that marshal torch tensors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -309,32 +310,73 @@ class Workspace:
         return self.buf.data_ptr()
 
 
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device, stream=None):
+    """A context with the tensors' device current (nothing to do in the usual case) and, where a stream is
+    given, that stream: what is allocated for the call then belongs to the stream the kernels run on, and its
+    memory goes to no other work before them."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a CUDA device, got {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return _NOTHING
+    return torch.cuda.device(device)
+
+
+def _handed(device, stream, *outputs):
+    """Outputs allocated on a given stream are for the caller's current one, too: once dropped, their memory
+    waits for both."""
+    import torch
+    here = torch.cuda.current_stream(device)
+    if here != stream:
+        for t in outputs:
+            t.record_stream(here)
+
+
 def forward(cfg, inputs: dict, y=None, workspace: Workspace | None = None, stream=None,
             topk_idx=None, topk_w=None, logits_out=None):
-    """Run moe_forward on device tensors; returns y [T, d] (allocated by torch if None)."""
+    """Run moe_forward on device tensors; returns y [T, d] (allocated by torch if None).
+
+    stream: the torch.cuda.Stream to run on (None: the current one).  Work on a given stream is ordered
+    by the caller: inputs ready on it, and kept, until the call has run; outputs read behind it."""
     import torch
     x = inputs["x"]
     shape, opts = shape_of(cfg), options_of(cfg)
-    if y is None:
-        y = torch.empty_like(x)
-    if workspace is None:
-        workspace = Workspace(moe_workspace_size(shape, opts), x.device)
-    st = (stream if stream is not None else torch.cuda.current_stream(x.device)).cuda_stream
-    tens = tensors_of(inputs, y, topk_idx, topk_w, logits_out)
-    _check(moe_forward(shape, opts, tens, workspace.ptr, workspace.nbytes, st))
+    made = []
+    with _on(x.device, stream):
+        if y is None:
+            y = torch.empty_like(x)
+            made.append(y)
+        if workspace is None:
+            workspace = Workspace(moe_workspace_size(shape, opts), x.device)
+        st = (stream if stream is not None else torch.cuda.current_stream(x.device)).cuda_stream
+        tens = tensors_of(inputs, y, topk_idx, topk_w, logits_out)
+        _check(moe_forward(shape, opts, tens, workspace.ptr, workspace.nbytes, st))
+    if stream is not None:
+        _handed(x.device, stream, *made)
     return y
 
 
 def route(cfg, inputs: dict, workspace: Workspace | None = None, stream=None):
-    """Run moe_route; returns (topk_idx [T, k] int32, topk_w [T, k] fp32)."""
+    """Run moe_route; returns (topk_idx [T, k] int32, topk_w [T, k] fp32).  stream: as for forward."""
     import torch
     logits = inputs["logits"] if inputs.get("logits") is not None else inputs["x"]
     shape, opts = shape_of(cfg), options_of(cfg)
-    idx = torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((cfg.T, cfg.k), dtype=torch.float32, device=logits.device)
-    if workspace is None:
-        workspace = Workspace(moe_workspace_size(shape, opts), logits.device)
-    st = (stream if stream is not None else torch.cuda.current_stream(logits.device)).cuda_stream
-    _check(moe_route(shape, opts, tensors_of(inputs, None, idx, w), workspace.ptr,
-                     workspace.nbytes, st))
+    dev = logits.device
+    with _on(dev, stream):
+        idx = torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=dev)
+        w = torch.empty((cfg.T, cfg.k), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = Workspace(moe_workspace_size(shape, opts), dev)
+        st = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+        _check(moe_route(shape, opts, tensors_of(inputs, None, idx, w), workspace.ptr,
+                         workspace.nbytes, st))
+    if stream is not None:
+        _handed(dev, stream, idx, w)
     return idx, w

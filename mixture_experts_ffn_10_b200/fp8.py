@@ -8,7 +8,8 @@ matrix product of ``include/moe_fp8.h``.
 The same operands as expert weights of the layer: ``w_dtype="fp8"`` with wq / ws as
 ``gate_up`` / ``gate_up_scales`` (``fp8.quantize_gate_up``) and ``down`` / ``down_scales``.
 Argument marshalling only: the work runs in the CUDA library, on the current stream of
-the tensors' device unless one is given.
+the tensors' device unless one is given (a torch.cuda.Stream, which the caller orders: inputs
+ready on it, and kept, until the call has run; outputs read behind it).
 """
 from __future__ import annotations
 
@@ -22,7 +23,6 @@ import mixture_experts_ffn_10_b200 as _m
 EXPORTED = ("moe_fp8_quantize", "moe_fp8_quantize_weights", "moe_fp8_matmul_workspace_size", "moe_fp8_matmul")
 BLOCK = 128
 
-_NOTHING = contextlib.nullcontext()
 _lib = None
 
 
@@ -42,13 +42,14 @@ def _library():
     return _lib
 
 
-def _on(device):
-    """A context with the tensors' device current (nothing to do in the usual case)."""
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a CUDA device, got {device}")
-    if device.index == torch.cuda.current_device():
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device, stream=None):
+    """The package's _on, without its call in the usual case."""
+    if stream is None and device.type == "cuda" and device.index == torch.cuda.current_device():
         return _NOTHING
-    return torch.cuda.device(device)
+    return _m._on(device, stream)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without its object: 2 us less
@@ -81,11 +82,13 @@ def quantize(x, stream=None):
     pitch = x.stride(0) if R > 1 else K
     if pitch < K:
         raise ValueError("the rows of x overlap")
-    with _on(x.device):
+    with _on(x.device, stream):
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
         s = x.new_empty((R, _cdiv(K, BLOCK)), dtype=torch.float32)
         _m._check(_library().moe_fp8_quantize(_dtype_code(x), R, K, x.data_ptr(), pitch, q.data_ptr(), s.data_ptr(),
                                               _stream(stream, x.device)))
+    if stream is not None:
+        _m._handed(x.device, stream, q, s)
     return q, s
 
 
@@ -96,11 +99,13 @@ def quantize_weights(w, stream=None):
         raise ValueError("w must be a contiguous [E, N, K] or [N, K]")
     *lead, N, K = w.shape
     E = lead[0] if lead else 1
-    with _on(w.device):
+    with _on(w.device, stream):
         q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
         s = torch.empty((*lead, _cdiv(N, BLOCK), _cdiv(K, BLOCK)), dtype=torch.float32, device=w.device)
         _m._check(_library().moe_fp8_quantize_weights(_dtype_code(w), E, N, K, w.data_ptr(), q.data_ptr(), s.data_ptr(),
                                                       _stream(stream, w.device)))
+    if stream is not None:
+        _m._handed(w.device, stream, q, s)
     return q, s
 
 
@@ -110,7 +115,9 @@ def quantize_gate_up(w, stream=None):
     E, F2, d = w.shape
     if F2 % 2:
         raise ValueError("a gate||up stack has an even number of rows")
-    q, s = quantize_weights(w.reshape(2 * E, F2 // 2, d), stream)
+    with _on(w.device, stream):  # (a stack that is not contiguous is copied)
+        halves = w.reshape(2 * E, F2 // 2, d)
+    q, s = quantize_weights(halves, stream)
     return q.view(E, F2, d), s.view(E, -1, s.shape[2])
 
 
@@ -138,15 +145,18 @@ def matmul(xq, xs, wq, ws, counts=None, y=None, workspace=None, stream=None):
     _operand("ws", ws, torch.float32, (*lead, _cdiv(N, BLOCK), nbk), dev)
     if counts is not None:
         _operand("counts", counts, torch.int32, (E,), dev)
-    with _on(dev):
+    if y is not None:
+        _operand("y", y, torch.bfloat16, (R, N), dev)
+    made = y is None
+    with _on(dev, stream):
         lib = _library()
-        if y is None:
+        if made:
             y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
-        else:
-            _operand("y", y, torch.bfloat16, (R, N), dev)
         if workspace is None:
             workspace = _m.Workspace(lib.moe_fp8_matmul_workspace_size(R, E, N, K), dev)
         _m._check(lib.moe_fp8_matmul(R, E, N, K, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
                                      None if counts is None else counts.data_ptr(), y.data_ptr(), workspace.ptr,
                                      workspace.nbytes, _stream(stream, dev)))
+    if made and stream is not None:
+        _m._handed(dev, stream, y)
     return y

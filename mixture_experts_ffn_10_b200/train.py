@@ -11,7 +11,8 @@ or step by step, without autograd:
     dlogits = train.router_backward(cfg, logits, idx, dw=dw, counts=counts, dloss=dloss, coef=0.01, seq_offsets=off)
 
 Argument marshalling only: the work runs in the CUDA library, on the current stream of the
-logits' device unless one is given.  cfg: any object with the attributes of a workload
+logits' device unless one is given (a torch.cuda.Stream, which the caller orders: inputs ready on
+it, and kept, until the call has run; outputs read behind it).  cfg: any object with the attributes of a workload
 configuration (T, E, k, score, renormalize, routed_scale, logit_dtype, ...).
 """
 from __future__ import annotations
@@ -90,7 +91,7 @@ def balance_loss(cfg, logits, idx, coef=1.0, seq_offsets=None, router_bias=None,
     autograd: ``route`` is, and ``router_backward`` is its gradient."""
     B = _check_inputs(cfg, logits, idx, seq_offsets, router_bias)
     dev = logits.device
-    with _on(dev):
+    with _on(dev, stream):
         lib, (shape, opts) = _library(), _config(cfg)
         counts = idx.new_empty((B, cfg.E))
         loss = logits.new_empty((), dtype=torch.float32)
@@ -107,6 +108,8 @@ def balance_loss(cfg, logits, idx, coef=1.0, seq_offsets=None, router_bias=None,
         _m._check(lib.moe_balance_loss(shape, opts, logits.data_ptr(), _ptr(router_bias), idx.data_ptr(), _ptr(seq_offsets), B,
                                        coef, counts.data_ptr(), loss.data_ptr(), workspace.ptr, workspace.nbytes,
                                        _stream(stream, dev)))
+    if stream is not None:
+        _m._handed(dev, stream, loss, counts)
     return loss, counts
 
 
@@ -123,12 +126,14 @@ def router_backward(cfg, logits, idx, dw=None, counts=None, dloss=None, coef=1.0
         _operand("counts", counts, torch.int32, (B, cfg.E), dev)
     if dloss is not None and (dloss.numel() != 1 or dloss.dtype != torch.float32 or dloss.device != dev):
         raise ValueError("dloss must be one fp32 value on the logits' device")
-    with _on(dev):
+    with _on(dev, stream):
         lib, (shape, opts) = _library(), _config(cfg)
         dlogits = torch.empty_like(logits)
         _m._check(lib.moe_router_backward(shape, opts, logits.data_ptr(), _ptr(router_bias), idx.data_ptr(), _ptr(dw),
                                           _ptr(counts), _ptr(seq_offsets), B, coef, _ptr(dloss), dlogits.data_ptr(),
                                           _stream(stream, dev)))
+    if stream is not None:
+        _m._handed(dev, stream, dlogits)
     return dlogits
 
 
