@@ -140,6 +140,9 @@ int check_tensors(const moe_shape* s, const moe_options* o, const moe_tensors* t
                        t->gate};
   for (const void* p : tma)
     if (p && !aligned16(p)) return fail(MOE_ERR_ALIGN, "x, weights, y and shared_output must be 16-byte aligned");
+  const uintptr_t elt = s->act_dtype == MOE_F32 ? 4 : 2;
+  for (const void* p : {t->gate_up_bias, t->down_bias, t->gate_bias})
+    if (reinterpret_cast<uintptr_t>(p) & (elt - 1)) return fail(MOE_ERR_ALIGN, "the biases must be aligned to their elements");
   if (t->y == t->x || (t->shared_output && t->y == t->shared_output))
     return fail(MOE_ERR_ARG, "y must not alias an input");
   return MOE_OK;

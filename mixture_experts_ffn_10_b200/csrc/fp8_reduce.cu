@@ -114,6 +114,19 @@ __device__ __forceinline__ void add_bf16x4(float4& acc, const uint16_t* p, float
   acc.w = fmaf(f, bf16_to_f32(v.y >> 16), acc.w);
 }
 
+// acc += bias[0 .. 3], which is aligned to its elements: a caller's bias may start anywhere
+// in a larger buffer, and its rows are a multiple of 16 long.
+__device__ __forceinline__ void add_bias4(float4& acc, const uint16_t* bias) {
+  if ((reinterpret_cast<uintptr_t>(bias) & 7u) == 0) {
+    add_bf16x4(acc, bias, 1.f);
+  } else {
+    acc.x += bf16_to_f32(__ldg(bias));
+    acc.y += bf16_to_f32(__ldg(bias + 1));
+    acc.z += bf16_to_f32(__ldg(bias + 2));
+    acc.w += bf16_to_f32(__ldg(bias + 3));
+  }
+}
+
 // Four outputs of one token per thread, slots in order.
 __global__ void __launch_bounds__(kThreads) combine_splits_kernel(Fp8CombineArgs a) {
   pdl_enter();
@@ -130,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) combine_splits_kernel(Fp8CombineArgs
     float4 v = sum4(a.partial + (int64_t)row * a.pitch + c, (int64_t)a.R * a.pitch, a.splits);
     if (a.bias) {
       const int e = a.idx[(int64_t)t * a.k + j];
-      if (e >= 0 && e < a.E) add_bf16x4(v, a.bias + (int64_t)e * a.d + c, 1.f);
+      if (e >= 0 && e < a.E) add_bias4(v, a.bias + (int64_t)e * a.d + c);
     }
     const float w = a.roww ? a.roww[row] : 1.f;
     acc.x = fmaf(w, v.x, acc.x);
