@@ -8,7 +8,8 @@
  * idx [T, k] (moe_route's, or any; an index outside [0, E) is a slot without an expert):
  *   p[t, e]  = softmax_e(l'[t])            (MOE_SCORE_SOFTMAX)
  *            = sigma(l'[t, e]) / sum_e sigma(l'[t, e])  (MOE_SCORE_SIGMOID)
- *              and 0 throughout for a row whose logits are all -inf;
+ *              and 0 throughout for a row whose logits l' are all -inf (sigmoid: all below
+ *              -700, as masks of the type's lowest value are);
  *   sequence b holds the tokens seq_offsets[b] .. seq_offsets[b + 1] - 1, n_b of them
  *              (NULL: one sequence of all T tokens; tokens outside every sequence are
  *              padding and enter nothing);

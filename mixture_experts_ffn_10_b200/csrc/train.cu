@@ -116,10 +116,17 @@ __device__ __forceinline__ void sigmoid_pair(float l, float* s, float* r) {
 }
 
 // What turns a logit into its score: softmax s = exp(l - m) inv_z, sigmoid s = sigma(l);
-// the share is s (softmax) or s inv_z.
+// the share is s (softmax) or s inv_z.  A far row of sigmoids: see scores().
 struct Norm {
   float m, inv_z;
+  bool far;
 };
+
+// Sigmoids of a row whose sum is below 2^-64 (every logit below -44) leave fp32 one after
+// the other from -87 down; but there sigma(l) = exp(l) to 2^-64 relative, so that their
+// shares are a softmax's: s = exp(l - m), 1 - sigma(l) = 1.  Rows that lie below -700
+// throughout (where the type's lowest value, a mask, lies) have no shares.
+constexpr float kFarSum = 0x1p-64f, kMaskedLogit = -700.f;
 
 // l' of the row in l[], scores in s[] (0 past E).  Whole warp.
 template <class L>
@@ -131,7 +138,7 @@ __device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& r
 #pragma unroll
     for (int n = 0; n < L::N; n++) l[n] += bias[n];
   }
-  Norm z{0.f, 0.f};
+  Norm z{0.f, 0.f, false};
   float sum = 0.f;
   if (a.score == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY;
@@ -152,6 +159,21 @@ __device__ __forceinline__ Norm scores(const RouterTrainArgs& a, const Row<L>& r
     }
   }
   sum = group_sum<L::G>(sum);
+  if (a.score != MOE_SCORE_SOFTMAX && __any_sync(0xffffffffu, sum < kFarSum)) {  // (rare)
+    float m = -INFINITY, far_sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < L::N; n++) m = fmaxf(m, l[n]);
+    m = group_max<L::G>(m);
+    z.far = sum < kFarSum && m >= kMaskedLogit;
+#pragma unroll
+    for (int n = 0; n < L::N; n++) {
+      const float x = fast_exp(l[n] - m);
+      far_sum += x;
+      if (z.far) s[n] = x;
+    }
+    far_sum = group_sum<L::G>(far_sum);
+    if (z.far) sum = far_sum;
+  }
   z.inv_z = sum == 0.f ? 0.f : 1.f / sum;
   if (a.score == MOE_SCORE_SOFTMAX) {
 #pragma unroll
@@ -482,6 +504,10 @@ __global__ void __launch_bounds__(kBackThreads, back_blocks(L::N)) router_backwa
         for (int n = 0; n < N; n++) {
           float se, r;
           sigmoid_pair(l[n], &se, &r);
+          if (z.far) {
+            se = s[n];
+            r = 1.f;
+          }
           d[n] = g * (cnt[n] - mean) * se * r;
         }
       }
