@@ -61,9 +61,11 @@ MOE_API int moe_balance_loss(const moe_shape *shape, const moe_options *opts, co
  *   dloss    [1] fp32 on the device, or NULL (1)
  *   dlogits  [T, E] logit_dtype, output: every element is written; computed in fp32 and
  *            rounded once
- * At least one of dw and counts is given.  With MOE_SCORE_SOFTMAX a row with a NaN or
- * +inf logit gives NaN; with MOE_SCORE_SIGMOID a NaN logit gives NaN where the formulas
- * depend on it.  Errors as above; T == 0 is a no-op. */
+ * At least one of dw and counts is given.  dw of a slot without an expert is not used.
+ * A row of which nothing enters (a token outside every sequence, or no counts, without a
+ * slot that has an expert or without dw) gives 0, whatever its logits.  Else, with
+ * MOE_SCORE_SOFTMAX a row with a NaN or +inf logit gives NaN; with MOE_SCORE_SIGMOID a NaN
+ * logit gives NaN where the formulas depend on it.  Errors as above; T == 0 is a no-op. */
 MOE_API int moe_router_backward(const moe_shape *shape, const moe_options *opts, const void *logits,
                                 const void *router_bias, const int32_t *idx, const float *dw, const int32_t *counts,
                                 const int32_t *seq_offsets, int64_t B, float coef, const float *dloss, void *dlogits,

@@ -399,8 +399,10 @@ __global__ void __launch_bounds__(kBackThreads, back_blocks(L::N)) router_backwa
       if (t < c1 && j < a.k) {
         const int64_t at = t * a.k + j;
         const int e = __ldg(a.idx + at);
+        const float dw = __ldg(a.dw + at);
+        // (a slot without an expert has no weight: its gradient may be anything, a NaN too)
         s.e[q] = (unsigned)e < (unsigned)a.E ? e : -1;
-        s.dw[q] = __ldg(a.dw + at);
+        s.dw[q] = s.e[q] >= 0 ? dw : 0.f;
       }
     }
   };
@@ -492,6 +494,12 @@ __global__ void __launch_bounds__(kBackThreads, back_blocks(L::N)) router_backwa
       const float less = fmaf(amp, mean, drop);
 #pragma unroll
       for (int n = 0; n < N; n++) d[n] = s[n] * fmaf(amp, cnt[n], -less);
+      // nothing of the row enters, whatever its logits (a padding token's may be a NaN)
+      const bool inert = amp == 0.f && drop == 0.f;
+      if (__any_sync(0xffffffffu, inert)) {
+#pragma unroll
+        for (int n = 0; n < N; n++) d[n] = inert ? 0.f : d[n];
+      }
     } else {
 #pragma unroll
       for (int n = 0; n < N; n++) d[n] = 0.f;
