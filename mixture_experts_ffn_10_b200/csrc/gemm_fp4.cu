@@ -260,9 +260,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) mma_commit(&tfull[acc]);
       }
+      // all issued MMAs complete before TMEM is released, and the last commit on every
+      // slot's barrier arrives before the CTA may exit (another commit's arrival does not
+      // tell that this one's has been made)
       mma_commit(drain);
       const uint64_t t0 = global_timer();
       while (!mbar_try_wait(drain, 0) && global_timer() - t0 < kTimeoutNs) {
+      }
+      for (uint32_t j = (it > (uint32_t)AST ? it - AST : 0); j < it; j++) {
+        while (!mbar_try_wait(&emptyA[j % AST], (j / AST) & 1) && global_timer() - t0 < kTimeoutNs) {
+        }
+      }
+      for (uint32_t j = (it > (uint32_t)WST ? it - WST : 0); j < it; j++) {
+        while (!mbar_try_wait(&emptyW[j % WST], (j / WST) & 1) && global_timer() - t0 < kTimeoutNs) {
+        }
       }
     }
   } else if (warp < 2 + kEpiWarps) {

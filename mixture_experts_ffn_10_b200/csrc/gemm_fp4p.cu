@@ -218,6 +218,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (!mbar_try_wait(&emptyA[j % AST], (j / AST) & 1) && global_timer() - t0 < kTimeoutNs) {
         }
       }
+      // and so for the decoded slots' barriers: a commit of each k-block arrives there, too
+      for (uint32_t j = (it > (uint32_t)WST ? it - WST : 0); j < it; j++) {
+        while (!mbar_try_wait(&emptyW[j % WST], (j / WST) & 1) && global_timer() - t0 < kTimeoutNs) {
+        }
+      }
     }
   } else if (warp == kCodesWarp) {
     // ------------------------------------------------------------ code producer (both CTAs, local)

@@ -32,10 +32,12 @@
 // bytes a clock: 770 clocks, the products 512) and by the power limit (clocks of 1.3 to
 // 1.65 GHz): 8192 rows of 8 experts of 4096 x 14336 1.80 ms, 1.6 PFLOP/s; 4096 rows of 32
 // experts of 7168 x 2048 0.37 ms; 8 rows by their weights, 59 us for 201 MB.
-// Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.  Launched in plain stream order,
-// and nothing starts before its end: as programmatic launches, a GEMM's CTAs started on SMs
-// that the GEMM before it left free, and 8 rows of 32 experts in a loop of calls ended in an
-// illegal address after some ten thousand (320 thousand calls without: none).
+// Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.  No asynchronous write into a
+// CTA's shared memory outlives it: its producer waits for every load and for the last commit
+// on every stage's barrier.  Launched in plain stream order, and nothing starts before its
+// end: as programmatic launches, without that wait, a GEMM's CTAs started on SMs that the
+// GEMM before it left free, and 8 rows of 32 experts in a loop of calls ended in an illegal
+// address.
 #include "fp8.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -382,15 +384,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // before the CTA may exit: every load issued has landed, and the last commit on every
-      // stage's barrier has arrived
+      // Before the CTA may exit: every load issued has landed, and the last commit on every
+      // stage's barrier has arrived (the drain barrier tells that the MMAs have ended, not
+      // that the arrivals of other commits have been made), also after a role has given up.
       const uint32_t n = issued < (uint32_t)stages ? issued : (uint32_t)stages;
+      const uint64_t t0 = global_timer();
       for (uint32_t j = issued - n; j < issued; j++) {
         const uint32_t at = 8 * (j % stages), parity = (j / stages) & 1;
-        uint64_t t0 = global_timer();
-        while (!try_wait(full + at, parity) && global_timer() - t0 < kTimeoutNs) {
+        while (!(try_wait(full + at, parity) && try_wait(empty + at, parity))) {
+          if (global_timer() - t0 > kTimeoutNs) {
+            set_status(p.status, MOE_ERR_TIMEOUT);
+            break;
+          }
         }
-        wait(empty + at, parity, abort, p.status);
       }
     } else if ((warp == 1 || warp == 3) && elect_one()) {
       // ---------------------------------------------------------- MMA issuers

@@ -431,10 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) mma_commit(&tfull[acc]);
       }
-      // all issued MMAs complete before TMEM is released
+      // all issued MMAs complete before TMEM is released, and the last commit on every
+      // stage's barrier arrives before the CTA may exit (another commit's arrival does not
+      // tell that this one's has been made)
       mma_commit(drain);
       const uint64_t t0 = global_timer();
       while (!mbar_try_wait(drain, 0) && global_timer() - t0 < kTimeoutNs) {
+      }
+      for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; j++) {
+        while (!mbar_try_wait(&empty[j % STAGES], (j / STAGES) & 1) && global_timer() - t0 < kTimeoutNs) {
+        }
       }
     }
   } else {
