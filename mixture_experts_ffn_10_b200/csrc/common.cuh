@@ -322,8 +322,8 @@ constexpr int kFp4GuBN = 64;      // h features per MXFP4 gate_up tile (64 gate 
 constexpr int kFp4DnBN = 128;     // output features per MXFP4 down tile
 
 // ---------------------------------------------------------------- programmatic dependent launch
-// Every kernel of the forward is launched with programmatic stream serialization:
-// it may be scheduled, and run a prologue that touches only shared memory, TMEM
+// Every kernel of the forward but the FP8 GEMMs and what reads their results (launch_ordered)
+// is launched with programmatic stream serialization: it may be scheduled, and run a prologue that touches only shared memory, TMEM
 // and its parameters, while the kernel before it in the stream still runs.
 // pdl_enter() must come before the kernel's first global-memory access: it
 // returns once the preceding kernel has completed with its writes visible, then

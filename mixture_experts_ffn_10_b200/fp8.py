@@ -9,7 +9,8 @@ The same operands as expert weights of the layer: ``w_dtype="fp8"`` with wq / ws
 ``gate_up`` / ``gate_up_scales`` (``fp8.quantize_gate_up``) and ``down`` / ``down_scales``.
 Argument marshalling only: the work runs in the CUDA library, on the current stream of
 the tensors' device unless one is given (a torch.cuda.Stream, which the caller orders: inputs
-ready on it, and kept, until the call has run; outputs read behind it).
+ready on it, and kept, until the call has run; outputs read behind it).  Nothing here is
+recorded by autograd: outputs of inputs that require a gradient have none.
 """
 from __future__ import annotations
 
