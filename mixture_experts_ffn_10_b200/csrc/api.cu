@@ -805,7 +805,7 @@ size_t make_plan(const moe_shape* s, const moe_options* o, Plan* p) {
   p->rows = p->R + (s->Fs > 0 ? s->T : 0);
   p->Fmax = s->Fs > s->F ? s->Fs : s->F;
   p->nchunks = cdiv(s->T, kChunkTokens);
-  // FP8: few rows sort in one block (77 rows: one launch of 6 us for three of 18)
+  // FP8: few rows sort in one block
   if (s->w_dtype == MOE_FP8 && p->R <= kFp8OneBlockRows) p->nchunks = 1;
   p->act_dtype = s->act_dtype;
   p->w_dtype = s->w_dtype;

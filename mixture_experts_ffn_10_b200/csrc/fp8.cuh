@@ -10,7 +10,11 @@ namespace moe {
 
 constexpr int kFp8Block = 128;    // columns (and weight rows) that share a scale
 constexpr int kFp8BM = 128;       // rows per tile of the FP8 grouped GEMM (UMMA M)
-constexpr int kFp8OneBlockRows = 512;  // routed rows that one block sorts
+// Routed rows that one block sorts: one launch for three, but one warp places the rows one
+// after the other.  The layer of 32 experts of 1024 x 512 with one expert a token, sorted by
+// one block and by three launches: 77 rows 33.0, 35.1 us, 128 rows 33.0, 33.0, 256 rows 34.2,
+// 33.0, 512 rows 40.2, 33.7.
+constexpr int kFp8OneBlockRows = 128;
 constexpr int kFp8MinNK = 16;     // K (and F) multiple: 16-byte rows
 
 // SMs of the current device.
