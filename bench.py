@@ -64,20 +64,20 @@ class L2Flush:
 # the hash of the code of that file and the headers it includes (kernel_sources_hash,
 # comments stripped) at capture time.
 # A figure whose hash is not the current sources' belongs to an older kernel: reported null.
-#   mixtral_bf16 gate_up: full-size capture (2.4584 GB read + 0.2333 GB written; other
-#     boxes read up to 2.84 GB: how many repeated weight-tile fetches hit L2 varies).
+#   mixtral_bf16 gate_up: full-size capture (2.5092 GB read + 0.2315 GB written; other
+#     boxes read 2.46 to 2.84 GB: how many repeated weight-tile fetches hit L2 varies).
 #   deepseek_bf16 gate_up: captured at E=32 T=1024 (same 256 routed rows per expert and one
-#     shared row per token, one eighth of every operand) and scaled by 8: 2.1469 GB read +
-#     0.0359 GB written per launch there.
-#   gptoss_mxfp4 gate_up: full-size capture, 0.3297 GB read + 0.0375 GB written.
+#     shared row per token, one eighth of every operand) and scaled by 8: 2.1431 GB read +
+#     0.0357 GB written per launch there.
+#   gptoss_mxfp4 gate_up: full-size capture, 0.3299 GB read + 0.0381 GB written.
 #   decode_T1 / decode_T8: the one launch of both GEMMs, full size (the fourth launch of
-#     that kernel): 0.3041 GB + 1.4 MB and 0.9444 GB + 1.2 MB.
+#     that kernel): 0.3041 GB + 3.9 MB and 0.9445 GB + 4.6 MB.
 NCU_TRAFFIC = {
-    ("mixtral_bf16", "gate_up"): (2458378496 + 233282048, "gemm_tcs.cu", "c30a86d32a81"),
-    ("deepseek_bf16", "gate_up"): (8 * (2146914048 + 35875072), "gemm_tcs.cu", "c30a86d32a81"),
-    ("gptoss_mxfp4", "gate_up"): (329699840 + 37458432, "gemm_fp4.cu", "af0ca3377e18"),
-    ("decode_T1", "gate_up"): (304128768 + 1417728, "gemm_tc.cu", "f397cb915a5e"),
-    ("decode_T8", "gate_up"): (944408832 + 1224192, "gemm_tc.cu", "f397cb915a5e"),
+    ("mixtral_bf16", "gate_up"): (2509188608 + 231484928, "gemm_tcs.cu", "ba6fc197728e"),
+    ("deepseek_bf16", "gate_up"): (8 * (2143138560 + 35732224), "gemm_tcs.cu", "ba6fc197728e"),
+    ("gptoss_mxfp4", "gate_up"): (329918208 + 38114560, "gemm_fp4.cu", "58cdf41bb6af"),
+    ("decode_T1", "gate_up"): (304086016 + 3889408, "gemm_tc.cu", "d03a123bb0f8"),
+    ("decode_T8", "gate_up"): (944508416 + 4646656, "gemm_tc.cu", "d03a123bb0f8"),
 }
 
 
