@@ -17,9 +17,9 @@
 //
 // Work: tiles of 128 rows by 256 weight rows (128 gate and their 128 up rows, or 256 plain
 // rows); persistent CTAs, one per SM; the tile list is made on the device from the groups'
-// row counts.  (On CTA pairs, 256 rows by 256 weight rows, the kernel loaded a third less
-// and was no faster: 8192 rows of 8 experts of 4096 x 14336 took 1.81 ms against 1.71, the
-// adds and the power limit being the bound.)  Warps of a CTA:
+// row counts.  (On CTA pairs, 256 rows by 256 weight rows, an earlier form of the kernel
+// loaded a third less and was no faster: 8192 rows of 8 experts of 4096 x 14336 took 1.81 ms
+// against 1.71.)  Warps of a CTA:
 //   0     TMA producer (128-byte swizzle, one block of K per stage);
 //   1, 3  MMA issue, blocks of K in turn; 1: TMEM, too;
 //   2     the products of row and weight scales, a ring of blocks ahead in shared memory
@@ -28,9 +28,10 @@
 //         fit 96 registers a thread, and four per scheduler hide the tensor memory reads
 //         (eight of 128 with registers handed over from the first four: 4096 rows 368 us
 //         against 366, 77 rows 119 against 123).
-// Large batches are bound by what a tile loads (48 KB per 128 x 256 x 128 from L2 at 64
-// bytes a clock: 770 clocks, the products 512) and by the power limit (clocks of 1.3 to
-// 1.65 GHz): 8192 rows of 8 experts of 4096 x 14336 1.80 ms, 1.6 PFLOP/s; 4096 rows of 32
+// Large batches: a block of K takes some 1200 clocks for 512 of products, and no unit is full
+// (6001 rows of 4096 x 4096: tensor pipe 47%, L2 39%, issue slots 57%, DRAM 23%); what is left
+// is the latency of the chain commit - barrier - reads and adds - hand-back, and the power
+// limit (clocks of 1.3 to 1.65 GHz): 8192 rows of 8 experts of 4096 x 14336 1.80 ms, 1.6 PFLOP/s; 4096 rows of 32
 // experts of 7168 x 2048 0.37 ms; 8 rows by their weights, 59 us for 201 MB.
 // Every wait is bounded (2 s) and reports MOE_ERR_TIMEOUT.  No asynchronous write into a
 // CTA's shared memory outlives it: its producer waits for every load and for the last commit

@@ -16,10 +16,11 @@
 // Backward, one launch: dl = J_w^T dw + A J_p^T c, with
 //   softmax:  dp/dl = p (1 - p'),  sigmoid: ds/dl = s (1 - s), p = s / Z,
 // the k slots of a token being added to its row in shared memory.
-// Bound by instructions for large batches, some 30 a value for the exponential, the sums and
-// the slots' detour: the loss of 32768 tokens, 256 experts and 24 sequences 18.7 us (2.8 at
-// the memory's rate; 5 of them the second launch), the gradient of 65536 tokens and 128
-// experts 22 us (5.8).  By latency for small ones: 100 tokens 8.4 and 6.0 us.
+// Large batches are bound by instructions, some 30 a value for the exponential, the sums and
+// the slots' detour, in half of the issue slots with a quarter to a third of the warps in
+// flight: the loss of 32768 tokens and 256 experts 16.8 us on the device (2.8 at the memory's
+// rate; 5 of them the second launch), the gradient of 65536 tokens and 128 experts 18.0 us
+// (softmax; 22.6 sigmoid; 5.8).  Small ones by latency: 100 tokens 9.0 and 3.8 us.
 #include "train.cuh"
 
 namespace moe {
