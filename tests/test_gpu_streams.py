@@ -108,21 +108,28 @@ def test_outputs_are_kept_for_the_callers_stream(moe, name):
     """An output of a given stream that the current stream still reads is no memory for the given stream's
     next calls."""
     call = _calls(moe, 3)[name]
-    side = torch.cuda.Stream()
-    torch.cuda.synchronize()
-    out = call(side)
-    torch.cuda.current_stream().wait_stream(side)
-    torch.cuda._sleep(DELAY)
-    read = [t.clone() for t in out]  # behind the delay
-    held = [t.data_ptr() for t in out]
-    sizes = [t.untyped_storage().nbytes() for t in out]
-    del out
-    with torch.cuda.stream(side):
-        again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
-        assert not {t.data_ptr() for t in again} & set(held)
-        for t in again:
-            t.fill_(0x7f)
     want = call(None)
-    for a, b in zip(read, want):
-        assert torch.equal(_bytes(a), _bytes(b))
+    side = torch.cuda.Stream()
+    for delay in (DELAY, 10 * DELAY, 40 * DELAY):
+        torch.cuda.synchronize()
+        out = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(delay)
+        read = [t.clone() for t in out]  # behind the delay
+        done = torch.cuda.Event()
+        done.record()
+        held = {t.data_ptr() for t in out}
+        sizes = [t.untyped_storage().nbytes() for t in out]
+        del out
+        with torch.cuda.stream(side):
+            again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+            pending = not done.query()  # (else the host was slower than the delay: a longer one)
+            assert not pending or not {t.data_ptr() for t in again} & held
+            for t in again:
+                t.fill_(0x7f)
+        for a, b in zip(read, want):
+            assert torch.equal(_bytes(a), _bytes(b))
+        if pending:
+            break
+    assert pending
     torch.cuda.synchronize()
